@@ -1,0 +1,452 @@
+// wf_batch_tables: block tables, slot maps and the attention's work list of a
+// batch of requests, built on the GPU from the requests' lengths, so that one
+// captured graph serves steps of any lengths and the host never waits for
+// them.
+//
+// With c_b cached and f_b new tokens of request b, pages of P tokens and
+// exclusive sums written E[.]:
+//   token_start_b = E[f]_b
+//   pages held h_b (given, or ceil(c_b / P)); needed n_b = max(h_b, ceil((c_b + f_b) / P))
+//   table[b][i] = free_pages[free_head + E[n - h]_b + i - h_b]   for h_b <= i < n_b
+//   new token i of b: local position x = c_b + i, position prefix_len + x,
+//   slot table[b][x / P] * P + x mod P
+//
+// One launch without any exchange between blocks: every block sums all
+// requests' lengths itself (one block-wide scan; a few KB from L2), block 0
+// writes the per-request results and the work list, the others each take a
+// share of the new tokens and find a token's request by bisection in shared
+// memory.  A thread whose token opens a page writes that page's table entry,
+// so nobody reads an entry that somebody else writes.  Bound by latency (launch, scan, bisection), not by
+// its few bytes.  All sums are 64-bit; what does not fit voids the whole step
+// (no tokens, no work, tables untouched) and is recorded in the plan.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "wf_batch.h"
+
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+
+struct TablesParams {
+  const int32_t* cached;
+  const int32_t* fresh;
+  const int32_t* prefix_len;
+  const int32_t* held;
+  const int32_t* free_pages;
+  const int32_t* free_head;
+  int32_t* free_head_out;
+  int32_t* held_out;
+  int32_t* table;
+  int32_t* token_start;
+  int32_t* slot_map;
+  int32_t* positions;
+  wf_batch_hdr* hdr;
+  wf_batch_unit* units;
+  int64_t* pre;    // exclusive sums of unit costs
+  int32_t* ctok;   // partial-row index of each token, -1 for none
+  int32_t B, max_tokens, cols, max_prefix, num_free, pool_pages;
+  int32_t page, page_shift, group, tile_tokens, block_tokens, kv_heads, max_ctas;
+  uint64_t fingerprint;
+};
+
+// Exclusive block-wide sums of N 64-bit values per thread; totals in `total`.
+template <int N>
+__device__ void block_scan(int64_t (&v)[N], int64_t (&total)[N], int64_t* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t inc[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    inc[k] = v[k];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, inc[k], off);
+      if (lane >= off) inc[k] += o;
+    }
+    if (lane == 31) scratch[k * kWarps + warp] = inc[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    int64_t w = scratch[k * kWarps + lane];  // every warp sums the warps' totals itself
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, w, off);
+      if (lane >= off) w += o;
+    }
+    total[k] = __shfl_sync(0xffffffffu, w, 31);
+    const int64_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+    v[k] = inc[k] - v[k] + (warp > 0 ? before : 0);
+  }
+  __syncthreads();  // scratch may be used again
+}
+
+// Last index i in [0, n) with a[i] <= x (a ascending, a[0] <= x).
+__device__ __forceinline__ int last_not_above(const int32_t* a, int n, int32_t x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= x)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int32_t ceil_shift(int64_t x, int s) { return int32_t((x + (int64_t(1) << s) - 1) >> s); }
+
+__global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesParams p) {
+  extern __shared__ int32_t sm[];
+  int32_t* s_start = sm;                // [B + 1] first token of each request
+  int32_t* s_first = s_start + p.B + 1; // [B] first new page of each request, from free_head
+  int32_t* s_ctok = s_first + p.B;      // [B] first partial-row token
+  int32_t* s_unit = s_ctok + p.B;       // [B + 1] first own unit (block 0)
+  __shared__ int64_t scratch[5 * kWarps];
+
+  const int tid = threadIdx.x;
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  const int Tt = p.tile_tokens;
+  const int32_t prefix = p.prefix_len ? *p.prefix_len : 0;
+  const int32_t head = *p.free_head;
+
+  // sums over requests: new tokens, new pages, tokens of one-tile units, own units, small requests
+  int64_t v[5] = {0, 0, 0, 0, 0}, total[5];
+  int bad = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int64_t c = p.cached[b], f = p.fresh[b];
+    const int64_t h = p.held ? p.held[b] : (c < 0 ? 0 : ceil_shift(c, p.page_shift));
+    if (c < 0 || f < 0 || h < (c < 0 ? 0 : ceil_shift(c, p.page_shift))) {
+      bad |= 1;
+      continue;
+    }
+    const int64_t n = max(h, int64_t(ceil_shift(c + f, p.page_shift)));
+    if (n > p.cols) {
+      bad |= 2;
+      continue;
+    }
+    const int64_t tiles = (f + Tt - 1) / Tt;
+    v[0] += f;
+    v[1] += n - h;
+    v[2] += (tiles & 1) ? f - (tiles - 1) * Tt : 0;
+    v[3] += (tiles + 1) / 2;
+    v[4] += f > 0 && 2 * f * p.group <= 128;
+  }
+  block_scan<5>(v, total, scratch);
+  if (prefix < 0 || head < 0) bad |= 1;
+  if (prefix > p.max_prefix || total[0] > p.max_tokens || head + total[1] > p.num_free) bad |= 2;
+  bad = (__syncthreads_or(bad & 1) ? 1 : 0) | (__syncthreads_or(bad & 2) ? 2 : 0);
+  if (bad) {
+    if (blockIdx.x == 0) {
+      for (int b = tid; b <= p.B; b += kThreads) p.token_start[b] = 0;
+      if (p.held_out)
+        for (int b = tid; b < p.B; b += kThreads) p.held_out[b] = p.held[b];
+      if (tid == 0) {
+        *p.free_head_out = head;
+        wf_batch_hdr h{};
+        h.status.code = (bad & 1) ? WF_ERR_INVALID_ARG : WF_ERR_CAPACITY;
+        h.fingerprint = p.fingerprint;
+        h.ctas = 1;
+        *p.hdr = h;
+        p.pre[0] = 0;
+      }
+    }
+    return;
+  }
+
+  // a request with few rows shares its prefix tiles with the others' (see batch_attn.cu)
+  const bool shared = prefix > 0 && total[4] >= 2;
+  for (int b = b0; b < b1; ++b) {
+    const int32_t c = p.cached[b], f = p.fresh[b];
+    const int32_t h = p.held ? p.held[b] : ceil_shift(c, p.page_shift);
+    const int32_t n = max(h, ceil_shift(int64_t(c) + f, p.page_shift));
+    const int32_t tiles = (f + Tt - 1) / Tt;
+    s_start[b] = int32_t(v[0]);
+    s_first[b] = int32_t(v[1]);
+    s_ctok[b] = int32_t(v[2]);
+    s_unit[b] = int32_t(v[3]);
+    if (blockIdx.x == 0) {
+      p.token_start[b] = int32_t(v[0]);
+      if (p.held_out) p.held_out[b] = n;
+    }
+    v[0] += f;
+    v[1] += n - h;
+    v[2] += (tiles & 1) ? f - (tiles - 1) * Tt : 0;
+    v[3] += (tiles + 1) / 2;
+  }
+  const int32_t tokens = int32_t(total[0]);
+  if (tid == 0) {
+    s_start[p.B] = tokens;
+    s_unit[p.B] = int32_t(total[3]);
+    if (blockIdx.x == 0) {
+      p.token_start[p.B] = tokens;
+      *p.free_head_out = head + int32_t(total[1]);
+    }
+  }
+  __syncthreads();
+
+  if (blockIdx.x > 0) {
+    for (int64_t t64 = int64_t(blockIdx.x - 1) * kThreads + tid; t64 < tokens; t64 += int64_t(gridDim.x - 1) * kThreads) {
+      const int32_t t = int32_t(t64);
+      const int b = last_not_above(s_start, p.B, t);
+      const int32_t i = t - s_start[b], c = p.cached[b], f = s_start[b + 1] - s_start[b];
+      const int32_t h = p.held ? p.held[b] : ceil_shift(c, p.page_shift);
+      const int32_t x = c + i, pi = x >> p.page_shift, in_page = x & (p.page - 1);
+      int32_t* entry = p.table + int64_t(b) * p.cols + pi;
+      int32_t pg;
+      if (pi >= h) {
+        pg = p.free_pages[head + s_first[b] + (pi - h)];
+        if (in_page == 0) *entry = pg;
+      } else {
+        pg = *entry;
+      }
+      // a page outside the pool gets no slot: the append skips it
+      p.slot_map[t] = pg >= 0 && pg < p.pool_pages ? pg * p.page + in_page : -1;
+      p.positions[t] = prefix + x;
+      const int32_t tiles = (f + Tt - 1) / Tt, tail = (tiles - 1) * Tt;
+      p.ctok[t] = (tiles & 1) && i >= tail ? s_ctok[b] + i - tail : -1;
+    }
+    return;
+  }
+
+  // ---- block 0: the attention's units and the running sum of their costs
+  const int32_t ptiles = (prefix + 127) >> 7;
+  const int32_t pair_tokens = 2 * Tt;
+  const int32_t np = shared ? (tokens + pair_tokens - 1) / pair_tokens : 0;
+  const int32_t own = s_unit[p.B];
+  for (int u = tid; u < np; u += kThreads) {
+    wf_batch_unit r;
+    r.req = -1;
+    r.tok0 = u * pair_tokens;
+    r.ntok = min(pair_tokens, tokens - r.tok0);
+    r.ktiles = 0;
+    r.ptiles = ptiles;
+    r.cbase = -1;
+    r.pos0 = 0;
+    r.len = 0;
+    p.units[u] = r;
+  }
+  for (int u = tid; u < own; u += kThreads) {
+    const int b = last_not_above(s_unit, p.B, u);
+    const int32_t c = p.cached[b], f = s_start[b + 1] - s_start[b], i0 = (u - s_unit[b]) * pair_tokens;
+    const bool small = shared && 2 * int64_t(f) * p.group <= 128;
+    wf_batch_unit r;
+    r.req = b;
+    r.tok0 = s_start[b] + i0;
+    r.ntok = min(pair_tokens, f - i0);
+    r.pos0 = c + i0;
+    r.len = c + f;
+    const int64_t last = int64_t(r.pos0) + r.ntok - 1;
+    const int64_t end = min(int64_t(r.len), (last / p.block_tokens + 1) * p.block_tokens);
+    r.ptiles = small ? -1 : ptiles;
+    r.ktiles = int32_t((end + 127) >> 7) + (small ? 0 : ptiles);
+    r.cbase = r.ntok <= Tt ? s_ctok[b] : -1;
+    p.units[np + u] = r;
+  }
+  __syncthreads();
+  // prefix units run only where a tile holds a token of a small request
+  if (shared)
+    for (int b = b0; b < b1; ++b) {
+      const int32_t s = s_start[b], f = s_start[b + 1] - s;
+      if (f > 0 && 2 * int64_t(f) * p.group <= 128)
+        for (int u = s / pair_tokens; u <= (s + f - 1) / pair_tokens; ++u) p.units[u].ktiles = ptiles;
+    }
+  __syncthreads();
+  int64_t carry = 0;
+  int32_t rows = 0;
+  for (int u0 = 0; u0 < np + own; u0 += kThreads) {
+    const int u = u0 + tid;
+    int64_t cost[1] = {0}, sum[1];
+    if (u < np + own) {
+      const int32_t kt = p.units[u].ktiles, nt = p.units[u].ntok;
+      cost[0] = kt == 0 ? 0 : int64_t(kt) * (nt > Tt ? WF_BATCH_PAIR_COST : WF_BATCH_SINGLE_COST) + WF_BATCH_UNIT_COST;
+      rows = max(rows, nt * p.group);
+    }
+    block_scan<1>(cost, sum, scratch);
+    if (u < np + own) p.pre[u] = carry + cost[0];
+    carry += sum[0];
+  }
+  for (int off = 16; off > 0; off >>= 1) rows = max(rows, __shfl_xor_sync(0xffffffffu, rows, off));
+  __shared__ int32_t s_rows;
+  if (tid == 0) s_rows = 0;
+  __syncthreads();
+  if ((tid & 31) == 0) atomicMax(&s_rows, rows);
+  __syncthreads();
+  if (tid == 0) {
+    p.pre[np + own] = carry;
+    wf_batch_hdr h{};
+    h.fingerprint = p.fingerprint;
+    h.tokens = tokens;
+    h.units = np + own;
+    h.prefix_units = np;
+    h.prefix_len = prefix;
+    h.max_rows = s_rows;
+    h.head_cost = carry;
+    // no CTA gets less than two single tiles: shorter shares cost more in merging than they save
+    const int64_t shares = carry * p.kv_heads / (2 * WF_BATCH_SINGLE_COST);
+    h.ctas = int32_t(max(int64_t(1), min(int64_t(p.max_ctas), shares)));
+    *p.hdr = h;
+  }
+}
+
+}  // namespace
+
+namespace wf {
+
+BatchLayout batch_layout(const wf_batch_desc* d) {
+  BatchLayout L{};
+  L.error = WF_ERR_INVALID_ARG;
+  if (!d) return L;
+  const int64_t H = d->num_heads, K = d->num_kv_heads, P = d->page_tokens;
+  if (H < 1 || K < 1 || H % K != 0 || d->pool_pages < 1 || d->max_requests < 1 || d->max_tokens < 1 ||
+      d->max_request_pages < 1 || d->max_prefix_pages < 0 || d->block_tokens < 1 || d->num_ctas < 0 || d->head_dim < 1)
+    return L;
+  if (d->dtype != WF_BF16 && d->dtype != WF_F32) return L;
+  if (P != 8 && P != 16 && P != 32 && P != 64 && P != 128) return L;
+  L.error = WF_ERR_UNSUPPORTED;
+  if (d->dtype != WF_BF16 || (d->head_dim != 64 && d->head_dim != 128) || H / K > 128) return L;
+  L.error = WF_ERR_CAPACITY;
+  // the work list's 64-bit cost arithmetic, int32 token and page indices
+  const int64_t kMaxKeys = int64_t(1) << 27;
+  if (K > 256 || H > 4096 || d->max_requests > 8192 || d->max_tokens > (1 << 22) || d->num_ctas > 256 ||
+      d->pool_pages * P > 0x7FFFFFFF || d->max_request_pages * P > kMaxKeys || d->max_prefix_pages * P > kMaxKeys)
+    return L;
+  L.ctas = d->num_ctas;
+  if (L.ctas == 0) {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      cudaGetLastError();
+      L.error = WF_ERR_CUDA;
+      return L;
+    }
+    L.ctas = sms < 256 ? sms : 256;
+  }
+  L.group = int32_t(H / K);
+  L.tile_tokens = 128 / L.group;
+  const int64_t pair = 2 * L.tile_tokens;
+  // own units: each request's tokens in pairs of tiles; prefix units: all tokens in pairs of tiles
+  L.max_units = int32_t(d->max_requests + d->max_tokens / pair + (d->max_tokens + pair - 1) / pair + 1);
+  const int64_t ctok = int64_t(d->max_requests) * L.tile_tokens;
+  L.max_ctok = ctok < d->max_tokens ? ctok : d->max_tokens;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  L.off_units = sizeof(wf_batch_hdr);
+  L.off_pre = up(L.off_units + size_t(L.max_units) * sizeof(wf_batch_unit));
+  L.off_ctok = up(L.off_pre + size_t(L.max_units + 1) * sizeof(int64_t));
+  L.plan_bytes = up(L.off_ctok + size_t(d->max_tokens) * sizeof(int32_t));
+  // partial rows: [prefix, own][key parity][ctok][H] and [ctas][head, tail][tile or key parity][128]
+  const size_t main_rows = size_t(4) * size_t(L.max_ctok) * size_t(H), cut_rows = size_t(L.ctas) * 4 * 128;
+  const size_t row = size_t(d->head_dim) * sizeof(float);
+  L.off_cut_o = up(WF_ATTN_STATUS_BYTES + main_rows * row);
+  L.off_main_lse = up(L.off_cut_o + cut_rows * row);
+  L.off_cut_lse = up(L.off_main_lse + main_rows * sizeof(float));
+  L.workspace_bytes = up(L.off_cut_lse + cut_rows * sizeof(float));
+  uint64_t f = 0xcbf29ce484222325ull;  // FNV-1a over the description's words
+  const int32_t words[] = {d->num_heads, d->num_kv_heads, d->head_dim, d->dtype, d->page_tokens, d->pool_pages,
+                           d->max_requests, d->max_tokens, d->max_request_pages, d->max_prefix_pages,
+                           d->block_tokens, L.ctas};
+  for (int32_t w : words)
+    for (int k = 0; k < 4; ++k) f = (f ^ uint64_t((uint32_t(w) >> (8 * k)) & 255)) * 0x100000001b3ull;
+  L.fingerprint = f | 1;  // never the zero of a plan that was not built
+  L.error = WF_OK;
+  return L;
+}
+
+}  // namespace wf
+
+extern "C" size_t wf_batch_plan_bytes(const wf_batch_desc* desc) {
+  const wf::BatchLayout L = wf::batch_layout(desc);
+  return L.error == WF_OK ? L.plan_bytes : 0;
+}
+
+extern "C" size_t wf_batch_workspace_bytes(const wf_batch_desc* desc) {
+  const wf::BatchLayout L = wf::batch_layout(desc);
+  return L.error == WF_OK ? L.workspace_bytes : 0;
+}
+
+extern "C" wf_status wf_batch_tables(const wf_batch_desc* desc, const int32_t* cached, const int32_t* fresh,
+                                     const int32_t* prefix_len, const int32_t* held, const int32_t* free_pages,
+                                     int32_t num_free, const int32_t* free_head, int32_t* free_head_out,
+                                     int32_t* held_out, int32_t* block_table, int32_t* token_start, int32_t* slot_map,
+                                     int32_t* positions, void* plan, size_t plan_bytes, wf_stream_t stream) {
+  const wf::BatchLayout L = wf::batch_layout(desc);
+  if (L.error != WF_OK) return L.error;
+  if (!cached || !fresh || (!free_pages && num_free > 0) || !free_head || !free_head_out || !block_table || !token_start || !slot_map ||
+      !positions || !plan || num_free < 0)
+    return WF_ERR_INVALID_ARG;
+  if (desc->max_prefix_pages > 0 && !prefix_len) return WF_ERR_INVALID_ARG;
+  if ((held == nullptr) != (held_out == nullptr)) return WF_ERR_INVALID_ARG;
+  // every block reads the lengths while block 0 writes: no output may be an input
+  const void* in[] = {cached, fresh, prefix_len, held, free_pages, free_head};
+  const void* out[] = {free_head_out, held_out, block_table, token_start, slot_map, positions, plan};
+  for (const void* i : in)
+    for (const void* o : out)
+      if (i && i == o) return WF_ERR_INVALID_ARG;
+  for (const void* x : in)
+    if (reinterpret_cast<uintptr_t>(x) % 4) return WF_ERR_ALIGNMENT;
+  for (const void* x : out)
+    if (reinterpret_cast<uintptr_t>(x) % 4) return WF_ERR_ALIGNMENT;
+  if (reinterpret_cast<uintptr_t>(plan) % 16) return WF_ERR_ALIGNMENT;
+  if (plan_bytes < L.plan_bytes) return WF_ERR_WORKSPACE;
+
+  TablesParams p{};
+  p.cached = cached;
+  p.fresh = fresh;
+  p.prefix_len = desc->max_prefix_pages > 0 ? prefix_len : nullptr;
+  p.held = held;
+  p.free_pages = free_pages;
+  p.free_head = free_head;
+  p.free_head_out = free_head_out;
+  p.held_out = held_out;
+  p.table = block_table;
+  p.token_start = token_start;
+  p.slot_map = slot_map;
+  p.positions = positions;
+  uint8_t* pl = static_cast<uint8_t*>(plan);
+  p.hdr = reinterpret_cast<wf_batch_hdr*>(pl);
+  p.units = reinterpret_cast<wf_batch_unit*>(pl + L.off_units);
+  p.pre = reinterpret_cast<int64_t*>(pl + L.off_pre);
+  p.ctok = reinterpret_cast<int32_t*>(pl + L.off_ctok);
+  p.B = desc->max_requests;
+  p.max_tokens = desc->max_tokens;
+  p.cols = desc->max_request_pages;
+  p.max_prefix = desc->max_prefix_pages * desc->page_tokens;
+  p.num_free = num_free;
+  p.pool_pages = desc->pool_pages;
+  p.page = desc->page_tokens;
+  while ((1 << p.page_shift) < p.page) ++p.page_shift;
+  p.group = L.group;
+  p.tile_tokens = L.tile_tokens;
+  p.block_tokens = desc->block_tokens;
+  p.kv_heads = desc->num_kv_heads;
+  p.max_ctas = L.ctas;
+  p.fingerprint = L.fingerprint;
+
+  const size_t smem = sizeof(int32_t) * (4 * size_t(p.B) + 2);
+  if (smem > 40 * 1024) {
+    static int attr_done[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return WF_ERR_CUDA;
+    if (dev < 0 || dev >= 64) return WF_ERR_UNSUPPORTED;
+    if (!attr_done[dev]) {
+      constexpr int kMost = int(sizeof(int32_t)) * (4 * 8192 + 2);
+      static_assert(kMost <= 227 * 1024 - 5 * kWarps * 8 - 16, "lengths in shared memory");
+      if (cudaFuncSetAttribute(batch_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess) {
+        cudaGetLastError();
+        return WF_ERR_CUDA;
+      }
+      attr_done[dev] = 1;
+    }
+  }
+  const int token_blocks = (p.max_tokens + kThreads - 1) / kThreads;
+  const int blocks = 1 + (token_blocks < 147 ? token_blocks : 147);
+  batch_tables_kernel<<<blocks, kThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
+}
+
+extern "C" wf_status wf_batch_status(const void* plan, wf_stream_t stream, int32_t* detail) {
+  return wf_attn_workspace_status(plan, stream, detail);  // the plan begins with the same status block
+}

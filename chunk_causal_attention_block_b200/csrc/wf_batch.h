@@ -1,0 +1,66 @@
+// Internal layout of the batch plan: the device buffer that wf_batch_tables
+// fills from request lengths on the GPU and that wf_batch_append and
+// wf_batch_attn read.  Nothing of it is known to the host, which only sizes
+// it from the capacities of wf_batch_desc.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "wf.h"
+#include "wf_plan.h"
+
+// Key tiles are shared out to CTAs by cost.  A tile against two row tiles
+// (256 rows) costs WF_BATCH_PAIR_COST, against one WF_BATCH_SINGLE_COST, and
+// every unit WF_BATCH_UNIT_COST more for filling and draining the pipeline.
+#define WF_BATCH_PAIR_COST 8
+#define WF_BATCH_SINGLE_COST 4
+#define WF_BATCH_UNIT_COST 4
+
+// One work unit of the attention, for one key head: up to two 128-row tiles of
+// queries (tokens tok0 .. tok0+ntok-1, each with the key head's query heads)
+// against ktiles 128-key tiles, the first ptiles of them the prefix's.
+struct wf_batch_unit {
+  int32_t req;     // request, or -1: rows of all requests against the prefix alone
+  int32_t tok0;    // first new token (row of q)
+  int32_t ntok;    // new tokens; more than a tile's tokens: two row tiles
+  int32_t ktiles;  // key tiles; 0: nothing to do
+  int32_t ptiles;  // prefix tiles at the front; -1: none, the rows' prefix part comes from a req -1 unit
+  int32_t cbase;   // partial-row index of token tok0 (units of one row tile), else -1
+  int32_t pos0;    // own position (without the prefix) of token tok0
+  int32_t len;     // own tokens of the request, cached and new
+};
+static_assert(sizeof(wf_batch_unit) == 32, "unit record layout");
+
+struct wf_batch_hdr {
+  wf_dev_status status;   // 0: what the table builder found wrong with the lengths (all zero: nothing)
+  uint64_t fingerprint;   // 16: of the description that the plan was built for
+  int32_t tokens;         // 24: new tokens of the step
+  int32_t units;          // 28: records in the unit list
+  int32_t prefix_units;   // 32: of them, the leading ones with req = -1
+  int32_t prefix_len;     // 36
+  int32_t ctas;           // 40: CTAs that the work is shared out to
+  int32_t max_rows;       // 44: most query rows (tokens x group) of any unit
+  int64_t head_cost;      // 48: cost of one key head's units
+  int32_t pad[50];
+};
+static_assert(sizeof(wf_batch_hdr) == 256, "batch plan header layout");
+
+namespace wf {
+
+// Sizes and offsets that follow from a description (valid if ok).
+struct BatchLayout {
+  wf_status error;
+  int32_t group;         // query heads per key head
+  int32_t tile_tokens;   // tokens of a 128-row tile: floor(128 / group)
+  int32_t ctas;
+  int32_t max_units;
+  int64_t max_ctok;      // capacity of partial-row tokens
+  size_t off_units, off_pre, off_ctok, plan_bytes;
+  size_t off_cut_o, off_main_lse, off_cut_lse, workspace_bytes;  // partial O first, after the status block
+  uint64_t fingerprint;
+};
+
+BatchLayout batch_layout(const wf_batch_desc* d);
+
+}  // namespace wf

@@ -33,6 +33,8 @@ EXPORTS = ("wf_plan_bytes", "wf_plan_round", "wf_balance_units", "wf_rope3d_appe
            "wf_attn_workspace_init", "wf_attn_workspace_status", "wf_chunk_causal_attn", "wf_rope3d_append_kv",
            "wf_chunk_causal_attn_rope",
            "wf_chunk_causal_attn_noalloc", "wf_attn_noalloc_status", "wf_quantize_fp8", "wf_chunk_causal_attn_fp8",
+           "wf_batch_plan_bytes", "wf_batch_workspace_bytes", "wf_batch_tables", "wf_batch_status",
+           "wf_batch_append", "wf_batch_attn",
            "wf_status_string", "wf_version", "wf_synth_fill")
 
 
@@ -54,6 +56,18 @@ class RoundDesc(ctypes.Structure):
         ("rope_theta", ctypes.c_double),
         ("dtype", ctypes.c_int32), ("num_ctas", ctypes.c_int32),
     ]
+
+
+class BatchDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_heads", "num_kv_heads", "head_dim", "dtype", "page_tokens", "pool_pages", "max_requests", "max_tokens",
+        "max_request_pages", "max_prefix_pages", "block_tokens", "num_ctas")]
+
+
+def make_batch_desc(H, Hkv, D, page_tokens, pool_pages, *, max_requests, max_tokens, max_request_pages,
+                    max_prefix_pages=0, block_tokens=1, dtype=WF_BF16, num_ctas=0) -> BatchDesc:
+    return BatchDesc(int(H), int(Hkv), int(D), int(dtype), int(page_tokens), int(pool_pages), int(max_requests),
+                     int(max_tokens), int(max_request_pages), int(max_prefix_pages), int(block_tokens), int(num_ctas))
 
 
 def make_desc(H, D, fh, fw, F, Wc, R, n0, noise_t: Sequence[int], *, S=0, pairs=(0, 0, 0),
@@ -100,6 +114,16 @@ def lib() -> ctypes.CDLL:
         L.wf_quantize_fp8.argtypes, L.wf_quantize_fp8.restype = [vp, vp, vp, vp, i32, vp], i32
         L.wf_chunk_causal_attn_fp8.argtypes = [vp] * 9 + [ctypes.c_float, vp, sz, vp]
         L.wf_chunk_causal_attn_fp8.restype = i32
+        bp = ctypes.POINTER(BatchDesc)
+        L.wf_batch_plan_bytes.argtypes, L.wf_batch_plan_bytes.restype = [bp], sz
+        L.wf_batch_workspace_bytes.argtypes, L.wf_batch_workspace_bytes.restype = [bp], sz
+        L.wf_batch_tables.argtypes = [bp] + [vp] * 5 + [i32] + [vp] * 8 + [sz, vp]
+        L.wf_batch_tables.restype = i32
+        L.wf_batch_status.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_int32)]
+        L.wf_batch_status.restype = i32
+        L.wf_batch_append.argtypes, L.wf_batch_append.restype = [bp] + [vp] * 10, i32
+        L.wf_batch_attn.argtypes = [bp] + [vp] * 8 + [ctypes.c_float, vp, sz, vp]
+        L.wf_batch_attn.restype = i32
         L.wf_status_string.argtypes, L.wf_status_string.restype = [i32], ctypes.c_char_p
         L.wf_version.argtypes, L.wf_version.restype = [], i32
         L.wf_synth_fill.argtypes = [vp, i32, u64, i32, i64, i64, i32, i32, i32, i32, i32, vp]
@@ -234,6 +258,70 @@ def wf_chunk_causal_attn_fp8(host_plan, dev_plan, q8, q_scales, k8_pool, k_scale
     _check(lib().wf_chunk_causal_attn_fp8(_ptr(host_plan), _ptr(dev_plan), _ptr(q8), _ptr(q_scales), _ptr(k8_pool),
                                           _ptr(k_scales), _ptr(v_pool), _ptr(out), _ptr(lse), float(softmax_scale),
                                           _ptr(workspace), wb, _stream(stream)), "wf_chunk_causal_attn_fp8")
+
+
+def wf_batch_plan_bytes(desc: BatchDesc) -> int:
+    return lib().wf_batch_plan_bytes(ctypes.byref(desc))
+
+
+def wf_batch_workspace_bytes(desc: BatchDesc) -> int:
+    return lib().wf_batch_workspace_bytes(ctypes.byref(desc))
+
+
+def _room(where, *args):
+    """(tensor, elements, element size): raises where a tensor is not dense or too small for what the call may touch.
+    Raw addresses and None pass: their owner vouches for them."""
+    for x, n, size in args:
+        if x is not None and not isinstance(x, (int, np.ndarray)) and (
+                not x.is_contiguous() or x.element_size() != size or x.numel() < n):
+            raise WfError(WF_ERR_INVALID_ARG, f"{where}: a tensor of {x.numel()} x {x.element_size()} bytes "
+                                              f"(contiguous: {x.is_contiguous()}) where {n} x {size} are needed")
+
+
+def wf_batch_tables(desc: BatchDesc, cached, fresh, prefix_len, free_pages, free_head, free_head_out, block_table,
+                    token_start, slot_map, positions, plan, held=None, held_out=None, stream=None, num_free=None,
+                    plan_bytes=None):
+    B = desc.max_requests
+    _room("wf_batch_tables", (cached, B, 4), (fresh, B, 4), (prefix_len, 1, 4), (free_pages, num_free or 0, 4),
+          (free_head, 1, 4), (free_head_out, 1, 4), (block_table, B * desc.max_request_pages, 4),
+          (token_start, B + 1, 4), (slot_map, desc.max_tokens, 4), (positions, desc.max_tokens, 4), (held, B, 4),
+          (held_out, B, 4))
+    nf = num_free if num_free is not None else free_pages.numel()
+    pb = plan_bytes if plan_bytes is not None else _nbytes(plan)
+    _check(lib().wf_batch_tables(ctypes.byref(desc), _ptr(cached), _ptr(fresh), _ptr(prefix_len), _ptr(held),
+                                 _ptr(free_pages), nf, _ptr(free_head), _ptr(free_head_out), _ptr(held_out),
+                                 _ptr(block_table), _ptr(token_start), _ptr(slot_map), _ptr(positions), _ptr(plan), pb,
+                                 _stream(stream)), "wf_batch_tables")
+
+
+def wf_batch_status(plan, stream=None):
+    """What wf_batch_tables found wrong with a step's lengths (a status code); synchronises `stream`."""
+    return lib().wf_batch_status(_ptr(plan), _stream(stream), None)
+
+
+def wf_batch_append(desc: BatchDesc, plan, slot_map, k, v, k_pool, v_pool, q=None, rope=None, q_rot=None, stream=None):
+    D, pool = desc.head_dim, desc.pool_pages * desc.page_tokens * desc.num_kv_heads * desc.head_dim
+    # the step may hold fewer tokens than max_tokens: only the device knows, so room for all is asked for
+    T = desc.max_tokens
+    _room("wf_batch_append", (slot_map, T, 4), (rope, T * D, 4), (q, T * desc.num_heads * D, 2),
+          (q_rot, T * desc.num_heads * D, 2), (k, T * desc.num_kv_heads * D, 2), (v, T * desc.num_kv_heads * D, 2),
+          (k_pool, pool, 2), (v_pool, pool, 2))
+    _check(lib().wf_batch_append(ctypes.byref(desc), _ptr(plan), _ptr(slot_map), _ptr(rope), _ptr(q), _ptr(k), _ptr(v),
+                                 _ptr(q_rot), _ptr(k_pool), _ptr(v_pool), _stream(stream)), "wf_batch_append")
+
+
+def wf_batch_attn(desc: BatchDesc, plan, block_table, prefix_table, q, k_pool, v_pool, out, lse=None,
+                  softmax_scale=0.0, workspace=None, stream=None, workspace_bytes=None):
+    D, pool = desc.head_dim, desc.pool_pages * desc.page_tokens * desc.num_kv_heads * desc.head_dim
+    T, H = desc.max_tokens, desc.num_heads
+    _room("wf_batch_attn", (block_table, desc.max_requests * desc.max_request_pages, 4),
+          (prefix_table, desc.max_prefix_pages, 4), (q, T * H * D, 2), (k_pool, pool, 2), (v_pool, pool, 2),
+          (out, T * H * D, 2), (lse, T * H, 4))
+    wb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
+    _check(lib().wf_batch_attn(ctypes.byref(desc), _ptr(plan), _ptr(block_table), _ptr(prefix_table), _ptr(q),
+                               _ptr(k_pool), _ptr(v_pool), _ptr(out), _ptr(lse), float(softmax_scale),
+                               _ptr(workspace), wb, _stream(stream)), "wf_batch_attn")
+
 
 def wf_synth_fill(dst, dtype, seed, tensor, tag, n_first, nchunks, C, H, D, kscale=False, stream=None):
     _check(lib().wf_synth_fill(_ptr(dst), int(dtype), int(seed) & 0xFFFFFFFFFFFFFFFF, int(tensor), int(tag),

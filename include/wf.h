@@ -357,6 +357,152 @@ wf_status wf_chunk_causal_attn_fp8(const void* host_plan, const void* dev_plan, 
                                    const void* v_pool, void* out, float* lse, float softmax_scale,
                                    void* workspace, size_t workspace_bytes, wf_stream_t stream);
 
+/*
+ * Batches of requests.  The calls above serve one stream whose lengths the
+ * host plans.  The three below serve a batch of requests -- branches of one
+ * history, candidates, prompts -- whose lengths live on the GPU: one captured
+ * graph serves steps of any lengths.  The pages have no counterpart: they
+ * describe one stream.
+ *
+ * Notation: H query heads, Hkv key heads (group = H / Hkv query heads share a
+ * key head, query head h reads key head h / group), D, pages of P tokens, B
+ * requests, T new tokens of the step (all requests' together, request by
+ * request), G block_tokens.  A request holds c_b cached tokens of its own in
+ * the pool and brings f_b new ones; its own positions are 0 .. c_b+f_b-1.
+ * All requests also see the same prefix, stored once.
+ *
+ * Layouts (dense, row-major): q, out [T, H, D]; k, v [T, Hkv, D]; K and V
+ * pools [pool_pages * P, Hkv, D], pool token p*P + i being token i of page p;
+ * block_table [B, max_request_pages], row b listing b's pages in order;
+ * prefix_table [max_prefix_pages] likewise.  Arrays of T entries have room for
+ * max_tokens; the calls leave what lies behind the step's T tokens as it was.
+ *
+ * Supported: bf16, D = 64 or 128, group up to 128, pages of 8, 16, 32, 64 or
+ * 128 tokens.  fp32 and other D return WF_ERR_UNSUPPORTED.
+ */
+typedef struct wf_batch_desc {
+  int32_t num_heads;         /* H >= 1 */
+  int32_t num_kv_heads;      /* Hkv in [1, 256], divides H */
+  int32_t head_dim;          /* D: 64 or 128 */
+  int32_t dtype;             /* WF_BF16 */
+  int32_t page_tokens;       /* P: 8, 16, 32, 64 or 128 */
+  int32_t pool_pages;        /* pages of the pool, pool_pages * P < 2^31 */
+  int32_t max_requests;      /* B in [1, 8192]; requests without new tokens are fine */
+  int32_t max_tokens;        /* most new tokens of a step, in [1, 2^22] */
+  int32_t max_request_pages; /* columns of the block table, at most 2^27 tokens */
+  int32_t max_prefix_pages;  /* entries of the prefix table, at most 2^27 tokens; 0: no prefix */
+  int32_t block_tokens;      /* G >= 1: see wf_batch_attn */
+  int32_t num_ctas;          /* CTAs of the attention, at most 256; 0 = SM count of the
+                                current device (needs a CUDA device) */
+} wf_batch_desc;
+
+/* Size in bytes of the device plan and of the attention workspace of `desc`
+ * (every step of it, whatever its lengths); 0 if `desc` is invalid. */
+size_t wf_batch_plan_bytes(const wf_batch_desc* desc);
+size_t wf_batch_workspace_bytes(const wf_batch_desc* desc);
+
+/*
+ * wf_batch_tables -- block tables, slot map and the step's plan, built on the
+ * GPU from the requests' lengths.
+ *
+ * Request b needs n_b = max(h_b, ceil((c_b + f_b) / P)) pages and holds h_b =
+ * held[b] (NULL: ceil(c_b / P)).  The missing ones are taken from free_pages,
+ * from index *free_head on, request by request, and written behind the held
+ * ones in its block-table row.  `held` serves steps whose cached length falls
+ * back below pages already taken (chunks denoised again, rejected proposals).
+ *
+ * cached, fresh: device int32 [B]: c_b >= 0, f_b >= 0.
+ * prefix_len:  device int32 [1]; may be NULL if max_prefix_pages is 0.
+ * held, held_out: device int32 [B]: pages held before and after; both or none.
+ * free_pages:  device int32 [num_free]; free_head: device int32 [1].
+ * free_head_out: device int32 [1] (written): *free_head + the pages taken.
+ * block_table: device int32 [B, max_request_pages] (entries h_b .. n_b-1 of
+ *              each row written, the others left as they were).
+ * token_start: device int32 [B + 1] (written): first new token of each request.
+ * slot_map, positions: device int32 [max_tokens] (the first T written): pool
+ *              token of each new token (-1 if its page lies outside the pool)
+ *              and its position prefix_len + c_b + i.
+ * plan:        device, >= wf_batch_plan_bytes(desc) bytes, 16-byte aligned.
+ * No output may be one of the inputs: every block reads the lengths while
+ * results are written (use *_out of one step as the input of the next).
+ *
+ * Lengths that are wrong (negative, held below the cached pages:
+ * WF_ERR_INVALID_ARG) or do not fit (max_tokens, block-table columns, prefix
+ * pages, free pages: WF_ERR_CAPACITY) are found on the GPU.  They void the
+ * whole step: no page is taken, block_table, slot_map and positions stay as
+ * they were, token_start is all 0, and the append and the attention of that
+ * plan do nothing.  wf_batch_status reads which it was.
+ * Errors: WF_ERR_INVALID_ARG, WF_ERR_UNSUPPORTED, WF_ERR_CAPACITY (the
+ * description), WF_ERR_ALIGNMENT, WF_ERR_WORKSPACE (plan too small), WF_ERR_CUDA.
+ */
+wf_status wf_batch_tables(const wf_batch_desc* desc, const int32_t* cached, const int32_t* fresh,
+                          const int32_t* prefix_len, const int32_t* held, const int32_t* free_pages,
+                          int32_t num_free, const int32_t* free_head, int32_t* free_head_out, int32_t* held_out,
+                          int32_t* block_table, int32_t* token_start, int32_t* slot_map, int32_t* positions,
+                          void* plan, size_t plan_bytes, wf_stream_t stream);
+
+/*
+ * What wf_batch_tables found wrong with the lengths of the step in `plan`
+ * (WF_OK, WF_ERR_INVALID_ARG or WF_ERR_CAPACITY); synchronises `stream`.
+ * `detail`, when non-NULL, receives 4 int32, the first of them the code.
+ */
+wf_status wf_batch_status(const void* plan, wf_stream_t stream, int32_t* detail);
+
+/*
+ * wf_batch_append -- writes the step's K and V rows into the pool at their
+ * slots; with `rope`, turns Q and K first.
+ *
+ * rope:  device fp32 [T, D/2, 2]: (cos, sin) of each interleaved pair
+ *        (x[2m], x[2m+1]) of each token, whatever positions or axes they come
+ *        from; x' = x cos - y sin, y' = x sin + y cos in fp32, rounded once
+ *        (nearest, ties to even).  NULL: K is copied; q and q_rot must be NULL.
+ * q, q_rot: device [T, H, D] (q_rot written; it may be q itself).
+ * k, v:  device [T, Hkv, D].
+ * slot_map: from wf_batch_tables; tokens whose slot lies outside the pool are
+ *        not stored.  Only slots of the step's tokens are written.
+ * plan:  of the same description; the call does nothing with another's.
+ * Errors: WF_ERR_INVALID_ARG, WF_ERR_UNSUPPORTED, WF_ERR_CAPACITY,
+ *         WF_ERR_ALIGNMENT, WF_ERR_CUDA.
+ */
+wf_status wf_batch_append(const wf_batch_desc* desc, const void* plan, const int32_t* slot_map, const float* rope,
+                          const void* q, const void* k, const void* v, void* q_rot, void* k_pool, void* v_pool,
+                          wf_stream_t stream);
+
+/*
+ * wf_batch_attn -- attention of the step's new tokens, the shared prefix read
+ * once for all requests with few rows.
+ *
+ * New token i of request b (own position x = c_b + i) sees the whole prefix
+ * and b's own keys [0, min(c_b + f_b, (x / G + 1) * G)): G = 1 is token-causal,
+ * G = the chunk length the chunk-causal mask of wf_chunk_causal_attn (chunks
+ * counted from the request's own position 0), G >= c_b + f_b full attention.
+ *   O = softmax(q K^T * scale) V,   LSE = ln sum exp(q K^T * scale)
+ * bf16 products on tensor cores with fp32 accumulation, P rounded to bf16
+ * before the PV product, O rounded once.  Every row sees at least its own key.
+ *
+ * block_table, prefix_table (NULL if max_prefix_pages is 0): pages of the keys;
+ *        the step's own K/V must be in the pool (wf_batch_append).  Entries
+ *        outside the pool read as zero keys and values.  Keys that a row may
+ *        see must be finite; whatever lies in a page behind a request's (or
+ *        the prefix's) last token is not used, NaN or not.
+ * out:   device [T, H, D] (written); lse: device fp32 [H, max_tokens] (the first T
+ *        of each row written), or NULL.
+ * softmax_scale: 0 means 1/sqrt(D).
+ * workspace: >= wf_batch_workspace_bytes(desc) bytes, its first 256 zeroed once
+ *        (wf_attn_workspace_init); it holds rows that are still to be merged, so
+ *        calls that may overlap on the GPU need one each.  Device errors are
+ *        read with wf_attn_workspace_status: WF_ERR_DEVICE_TIMEOUT, or
+ *        WF_ERR_PLAN if the plan was not built for this description (nothing
+ *        is written then).
+ * The result does not depend on timing: parts are merged in a fixed order.
+ * Errors: WF_ERR_INVALID_ARG, WF_ERR_UNSUPPORTED, WF_ERR_CAPACITY,
+ *         WF_ERR_ALIGNMENT, WF_ERR_WORKSPACE, WF_ERR_CUDA.
+ */
+wf_status wf_batch_attn(const wf_batch_desc* desc, const void* plan, const int32_t* block_table,
+                        const int32_t* prefix_table, const void* q, const void* k_pool, const void* v_pool, void* out,
+                        float* lse, float softmax_scale, void* workspace, size_t workspace_bytes,
+                        wf_stream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* wf_status_string(wf_status status);
 
