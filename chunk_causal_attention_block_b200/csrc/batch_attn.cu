@@ -29,7 +29,7 @@
 //
 // Warp roles (384 threads; registers as in attn_sm100.cu):
 //   warps 0-3, 4-7  softmax of stream 0 and 1
-//   warp  8   MMA issue (lane 0), TMEM allocation
+//   warp  8   MMA issue (one elected lane), TMEM allocation
 //   warp  9   TMA producer: Q tiles (ring of two), K/V pages (ring of kStages)
 //   warp 10   scheduler: walks this CTA's share and publishes items
 //   warp 11   zeroes the V rows behind a list's last key, whatever the page
@@ -43,6 +43,7 @@
 #include <cudaTypedefs.h>
 
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
 #include <cstdlib>
 
@@ -79,15 +80,16 @@ struct Params {
   const wf_batch_unit* units;
   const int64_t* pre;
   const int32_t* ctok;
+  const wf_batch_ctok* ctok_list;
   const int32_t* table;
   const int32_t* prefix_table;
   __nv_bfloat16* out;
   float* lse;
   wf_dev_status* status;
-  float* main_o;
-  float* cut_o;
-  float* main_lse;
-  float* cut_lse;
+  float* part_o;    // partial rows: [prefix, own][key parity][ctok][H], then [CTA][head, tail][row tile or key parity][128]
+  float* part_lse;
+  int2* cuts;       // per CTA: (key head, unit) that its first item continues, unit -1 for none
+  int64_t main_rows;
   uint64_t fingerprint;
   uint64_t timeout_ns;
   float scale_log2;
@@ -174,23 +176,46 @@ __device__ __forceinline__ bool warp_wait(const Shared& sh, const Params& p, int
 }
 
 // ---------------------------------------------------------------- shares of the line of costs
-__device__ __forceinline__ int64_t share_begin(int c, int64_t total, int ctas) { return int64_t(c) * total / ctas; }
+// Equal shares of `size` (the last one shorter); the division by it is a
+// multiplication by floor((2^64 - 1) / size), at most one below the quotient.
+struct Line {
+  int64_t head_cost, total, size;
+  uint64_t inv;
+};
 
-// The share that holds cost position x.
-__device__ __forceinline__ int share_of(int64_t x, int64_t total, int ctas) {
-  return int(((x + 1) * ctas + total - 1) / total) - 1;
+__device__ __forceinline__ Line line_of(const Params& p) {
+  const wf_batch_hdr* h = p.hdr;
+  Line x;
+  x.head_cost = h->head_cost;
+  x.total = h->head_cost * p.kv_heads;
+  x.size = h->share;
+  x.inv = h->share_inv;
+  return x;
 }
 
-// Key tiles of a unit at cost position s (cost w per tile) that start inside [lo, hi).
+__device__ __forceinline__ int64_t share_begin(const Line& x, int c) {
+  const int64_t b = c * x.size;
+  return b < x.total ? b : x.total;
+}
+
+// The share that holds cost position s < total.
+__device__ __forceinline__ int share_of(const Line& x, int64_t s) {
+  int c = int(__umul64hi(uint64_t(s), x.inv));
+  c += (c + 1) * x.size <= s;
+  return c;
+}
+
+// Key tiles of a unit at cost position s (1 << w per tile) that start inside [lo, hi).
 __device__ __forceinline__ void share_tiles(int64_t s, int32_t w, int32_t ktiles, int64_t lo, int64_t hi, int32_t& j0,
                                             int32_t& j1) {
-  const int64_t a = lo <= s ? 0 : (lo - s + w - 1) / w, b = hi <= s ? 0 : (hi - s + w - 1) / w;
+  const int64_t up = (int64_t(1) << w) - 1;
+  const int64_t a = lo <= s ? 0 : (lo - s + up) >> w, b = hi <= s ? 0 : (hi - s + up) >> w;
   j0 = int32_t(a < ktiles ? a : ktiles);
   j1 = int32_t(b < ktiles ? b : ktiles);
 }
 
-__device__ __forceinline__ int32_t tile_cost(int32_t ntok, int32_t tile_tokens) {
-  return ntok > tile_tokens ? WF_BATCH_PAIR_COST : WF_BATCH_SINGLE_COST;
+__device__ __forceinline__ int32_t tile_shift(int32_t ntok, int32_t tile_tokens) {
+  return ntok > tile_tokens ? WF_BATCH_PAIR_SHIFT : WF_BATCH_SINGLE_SHIFT;
 }
 
 // Whether rows of this unit run no other key tiles than the unit's, and on one
@@ -199,18 +224,50 @@ __device__ __forceinline__ bool unit_direct(const wf_batch_unit& u, int32_t tile
   return u.req >= 0 && u.ptiles >= 0 && (u.ntok > tile_tokens || u.ktiles == 1);
 }
 
+// Indices of partial rows.
+__device__ __forceinline__ int64_t main_row(const Params& p, bool own, int key_parity, int32_t ctok, int32_t head) {
+  return (int64_t((own ? 2 : 0) + key_parity) * p.max_ctok + ctok) * p.H + head;
+}
+__device__ __forceinline__ int64_t cut_row(const Params& p, int cta, bool tail, int half, int32_t row) {
+  return p.main_rows + ((int64_t(cta) * 2 + tail) * 2 + half) * 128 + row;
+}
+
 // ---------------------------------------------------------------- item ring
 // Copies item `it` and gives its slot back; false at the end (or on an abort).
-// Called by whole warps, and with kLane by one lane alone.
-template <int D, bool kLane = false>
+// The fields come through a shuffle from lane 0, which tells the compiler that
+// they are the same in all lanes: what the MMA and the producer warp derive
+// from them (loop counts, ring positions, descriptors) then stays in uniform
+// registers, as tcgen05.mma and TMA instructions need it.  Without that each
+// MMA took 136 cycles to issue instead of 64 (its operands moved from ordinary
+// registers one by one).
+template <int D>
 __device__ __forceinline__ bool take_item(const Shared& sh, const Params& p, int it, Item& x, int where) {
-  const int bar = Cfg<D>::kItemFull + it % kItems;
-  const uint32_t parity = (it / kItems) & 1;
-  if (!(kLane ? wait_bar(sh, p, bar, parity, where) : warp_wait(sh, p, bar, parity, where))) return false;
-  x = sh.items[it % kItems];
-  if (!kLane) __syncwarp();
-  if (kLane || (threadIdx.x & 31) == 0) mbar_arrive(smem_u32(sh.bars + Cfg<D>::kItemEmpty + it % kItems));
+  if (!warp_wait(sh, p, Cfg<D>::kItemFull + it % kItems, (it / kItems) & 1, where)) return false;
+  const int32_t* src = reinterpret_cast<const int32_t*>(sh.items + it % kItems);
+  int32_t* dst = reinterpret_cast<int32_t*>(&x);
+#pragma unroll
+  for (int k = 0; k < int(sizeof(Item) / 4); ++k) dst[k] = __shfl_sync(0xffffffffu, src[k], 0);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(sh.bars + Cfg<D>::kItemEmpty + it % kItems));
   return x.j1 > 0;
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes != 0;
+}
+
+__device__ __forceinline__ int32_t item_field(uint32_t item, uint32_t offset) {
+  return int32_t(ld_shared_u32(item + offset));
+}
+
+// The whole warp is done with item `it`.
+template <int D>
+__device__ __forceinline__ void release_item(const Shared& sh, int it) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(sh.bars + Cfg<D>::kItemEmpty + it % kItems));
 }
 
 template <int D>
@@ -218,12 +275,13 @@ __device__ __forceinline__ void scheduler(const Shared& sh, const Params& p) {
   const int lane = threadIdx.x & 31;
   int it = 0;
   int32_t parity = 0;
-  const wf_batch_hdr* h = p.hdr;
-  const int64_t head_cost = h->head_cost, total = head_cost * p.kv_heads;
-  const int ctas = h->ctas, units = h->units;
+  int32_t cut_unit = -1, cut_head = 0;
+  const Line line = line_of(p);
+  const int64_t head_cost = line.head_cost;
+  const int units = p.hdr->units;
   const int c = int(blockIdx.x);
-  if (h->fingerprint == p.fingerprint && total > 0 && c < ctas) {
-    const int64_t lo = share_begin(c, total, ctas), hi = share_begin(c + 1, total, ctas);
+  const int64_t lo = share_begin(line, c), hi = share_begin(line, c + 1);
+  if (p.hdr->fingerprint == p.fingerprint && lo < hi) {
     int32_t head = int32_t(lo / head_cost);
     // first unit: the last one that starts at or before lo, found 32 probes at a time
     const int64_t rem = lo - int64_t(head) * head_cost;
@@ -249,7 +307,7 @@ __device__ __forceinline__ void scheduler(const Shared& sh, const Params& p) {
         s = int64_t(head) * head_cost + __ldg(p.pre + mine);
       }
       int32_t j0 = 0, j1 = 0;
-      const int32_t w = tile_cost(r.ntok, p.tile_tokens);
+      const int32_t w = tile_shift(r.ntok, p.tile_tokens);
       if (mine < units) share_tiles(s, w, r.ktiles, lo, hi, j0, j1);
       const uint32_t live = __ballot_sync(0xffffffffu, mine < units && j0 < j1);
       more = __all_sync(0xffffffffu, mine >= units || s < hi);
@@ -279,6 +337,10 @@ __device__ __forceinline__ void scheduler(const Shared& sh, const Params& p) {
                                                    : kMainOwn;
           sh.items[it % kItems] = x;
           mbar_arrive(smem_u32(sh.bars + Cfg<D>::kItemFull + it % kItems));
+          if (j0 > 0) {
+            cut_unit = mine;
+            cut_head = head;
+          }
         }
         __syncwarp();
         parity = (parity + n) & 1;
@@ -293,6 +355,9 @@ __device__ __forceinline__ void scheduler(const Shared& sh, const Params& p) {
       }
     }
   }
+  // only the first item can continue a unit
+  if (const uint32_t who = __ballot_sync(0xffffffffu, cut_unit >= 0); who ? lane == __ffs(who) - 1 : lane == 0)
+    p.cuts[c] = make_int2(cut_head, cut_unit);
   if (!warp_wait(sh, p, Cfg<D>::kItemEmpty + it % kItems, ((it / kItems) & 1) ^ 1, 41)) return;
   if (lane == 0) {
     Item x{};
@@ -302,44 +367,54 @@ __device__ __forceinline__ void scheduler(const Shared& sh, const Params& p) {
 }
 
 // ---------------------------------------------------------------- K/V tiles
-// Key tile j of an item: where its pages are listed and how many keys it holds.
+// Key tile j of an item.  Lane i of the producer holds the first pool token of
+// the tile's i-th page (16 at most): read from the table once, a tile ahead of
+// its use, for K and V both.
 struct KeyTile {
   int32_t head;
   int32_t valid;   // keys, at most 128
-  int32_t own;     // 1: block table, 0: prefix table
-  int64_t entry;   // first page's entry there
+  int32_t at;      // of this lane's page
 };
+
+__device__ __forceinline__ int32_t tile_keys(const Item& x, int32_t j, int32_t prefix_len) {
+  const int32_t left = j >= x.ptiles ? x.len - (j - x.ptiles) * 128 : prefix_len - j * 128;
+  return left < 128 ? left : 128;
+}
 
 __device__ __forceinline__ KeyTile key_tile(const Params& p, const Item& x, int32_t j, int32_t prefix_len) {
   KeyTile k;
   k.head = x.head;
-  k.own = j >= x.ptiles;
-  const int32_t base = (k.own ? j - x.ptiles : j) * 128;
-  const int32_t left = (k.own ? x.len : prefix_len) - base;
-  k.valid = left < 128 ? left : 128;
-  k.entry = (k.own ? int64_t(x.req) * p.cols : 0) + (base >> p.page_shift);
+  k.valid = tile_keys(x, j, prefix_len);
+  const bool own = j >= x.ptiles;
+  const int32_t pg = int32_t(threadIdx.x & 31);
+  const int32_t* list = own ? p.table + x.req * p.cols : p.prefix_table;
+  const int32_t first = ((own ? j - x.ptiles : j) * 128) >> p.page_shift;
+  k.at = 0;
+  if (pg << p.page_shift < k.valid) {
+    // an entry outside the pool reads zeros, not memory: the map's bounds hold
+    const int64_t tok = int64_t(__ldg(list + first + pg)) << p.page_shift;
+    k.at = tok < 0 || tok > 0x7FFFFF00 ? 0x7FFFFF00 : int32_t(tok);
+  }
   return k;
 }
 
-// The whole warp copies a tile's pages, one (page, 64-column half) per lane and
-// round; only pages that hold keys are read.
+// Copies a tile; only pages that hold keys are read.  The pages go round by
+// shuffle and one lane issues all copies (32 lanes issuing one each serialise,
+// at about 85 cycles a copy).
 template <int D>
 __device__ __forceinline__ void load_tile(const Shared& sh, const Params& p, const CUtensorMap* tm, const KeyTile& k,
                                           int st, int bar_index) {
-  const int lane = threadIdx.x & 31;
   const int pages = (k.valid + (1 << p.page_shift) - 1) >> p.page_shift;
   const uint32_t page_bytes = 128u << p.page_shift;  // of one half
   const uint32_t bar = smem_u32(sh.bars + bar_index);
-  if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(pages) * page_bytes * Cfg<D>::kHalves);
-  __syncwarp();
-  const int32_t* list = k.own ? p.table : p.prefix_table;
-  const uint32_t dst = smem_u32(kv_tile<D>(sh, st));
-  for (int i = lane; i < pages * Cfg<D>::kHalves; i += 32) {
-    const int pg = i / Cfg<D>::kHalves, half = i % Cfg<D>::kHalves;
-    // an entry outside the pool reads zeros, not memory: the map's bounds hold
-    const int64_t tok = int64_t(__ldg(list + k.entry + pg)) << p.page_shift;
-    const int32_t at = tok < 0 || tok > 0x7FFFFF00 ? 0x7FFFFF00 : int32_t(tok);
-    tma_load_3d(dst + half * kHalfBytes + pg * page_bytes, tm, bar, 64 * half, k.head, at);
+  uint32_t dst = smem_u32(kv_tile<D>(sh, st));
+  if (elect_one()) mbar_arrive_expect_tx(bar, uint32_t(pages) * page_bytes * Cfg<D>::kHalves);
+  for (int pg = 0; pg < pages; ++pg, dst += page_bytes) {
+    const int32_t at = __shfl_sync(0xffffffffu, k.at, pg);
+    if (elect_one()) {
+      tma_load_3d(dst, tm, bar, 0, k.head, at);
+      if (Cfg<D>::kHalves == 2) tma_load_3d(dst + kHalfBytes, tm, bar, 64, k.head, at);
+    }
   }
 }
 
@@ -351,7 +426,6 @@ template <int D>
 __device__ __forceinline__ void producer(const Shared& sh, const Params& p, const CUtensorMap* tm_q,
                                          const CUtensorMap* tm_k, const CUtensorMap* tm_v) {
   using C = Cfg<D>;
-  const int lane = threadIdx.x & 31;
   const int32_t prefix_len = p.hdr->prefix_len;
   int kv_it = 0, q_it = 0;
   uint32_t raw_phase = 0, raw_last = 0;  // per stage: parity of the next raw fill; last fill was raw
@@ -374,19 +448,24 @@ __device__ __forceinline__ void producer(const Shared& sh, const Params& p, cons
   int it = 0;
   Item x;
   for (; ok && take_item<D>(sh, p, it, x, 1); ++it) {
+    KeyTile next = key_tile(p, x, x.j0, prefix_len);
     const int tiles = x.ntok > p.tile_tokens ? 2 : 1;
     for (int s = 0; s < tiles && ok; ++s, ++q_it) {
       const int slot = q_it & 1;
       if (!warp_wait(sh, p, C::kQEmpty + slot, ((q_it >> 1) & 1) ^ 1, 3)) { ok = false; break; }
       const uint32_t bar = smem_u32(sh.bars + C::kQFull + slot);
-      if (lane == 0) mbar_arrive_expect_tx(bar, q_bytes);
+      if (elect_one()) {
+        mbar_arrive_expect_tx(bar, q_bytes);
+#pragma unroll
+        for (int half = 0; half < C::kHalves; ++half)
+          tma_load_3d(smem_u32(q_tile<D>(sh, slot)) + half * kHalfBytes, tm_q, bar, 64 * half, x.head * p.group,
+                      x.tok0 + s * p.tile_tokens);
+      }
       __syncwarp();
-      if (lane < C::kHalves)
-        tma_load_3d(smem_u32(q_tile<D>(sh, slot)) + lane * kHalfBytes, tm_q, bar, 64 * lane, x.head * p.group,
-                    x.tok0 + s * p.tile_tokens);
     }
     for (int j = x.j0; j < x.j1 && ok; ++j) {
-      const KeyTile k = key_tile(p, x, j, prefix_len);
+      const KeyTile k = next;
+      if (j + 1 < x.j1) next = key_tile(p, x, j + 1, prefix_len);
       for (int s = 0; s < tiles && ok; ++s) {
         if (has2 && !fill(tm_v, v2, true)) ok = false;
         if (ok && s == 0 && !fill(tm_k, k, false)) ok = false;
@@ -457,7 +536,7 @@ __device__ __forceinline__ void zero_role(const Shared& sh, const Params& p) {
   for (int it = 0; take_item<D>(sh, p, it, x, 51); ++it) {
     const int tiles = x.ntok > p.tile_tokens ? 2 : 1;
     for (int j = x.j0; j < x.j1; ++j) {
-      const int32_t valid = key_tile(p, x, j, prefix_len).valid;
+      const int32_t valid = tile_keys(x, j, prefix_len);
       for (int s = 0; s < tiles; ++s) {
         if (!pass_v(v2)) return;
         kv_it += s == 0;
@@ -504,21 +583,24 @@ __device__ __forceinline__ void mma_issuer(const Shared& sh, const Params& p, ui
     const uint32_t t = m & 1;
     if (pv & kPvOpens) {
       vst = kv_it % C::kStages;
-      if (!wait_bar(sh, p, C::kKVFull + vst, (kv_it / C::kStages) & 1, 12)) return false;
+      if (!warp_wait(sh, p, C::kKVFull + vst, (kv_it / C::kStages) & 1, 12)) return false;
       ++kv_it;
     }
-    if (!wait_bar(sh, p, C::kPFull + t, (p_phase >> t) & 1, 14 + t)) return false;
+    if (!warp_wait(sh, p, C::kPFull + t, (p_phase >> t) & 1, 14 + t)) return false;
     p_phase ^= 1u << t;
     tc_fence_after();
-    issue_pv_slice<D, 0>(tmem + 256 + 128 * t, tmem + 128 * t,
-                         smem_desc_sw128(smem_u32(kv_tile<D>(sh, vst)), kHalfBytes, 1024), pv & kPvFirst ? 0u : 1u);
-    if (pv & kPvLast) mma_commit(smem_u32(sh.bars + C::kOFull + t));
-    if (pv & kPvCloses) mma_commit(smem_u32(sh.bars + C::kKVEmpty + vst));
+    const uint64_t vd = smem_desc_sw128(smem_u32(kv_tile<D>(sh, vst)), kHalfBytes, 1024);
+    if (elect_one()) {
+      issue_pv_slice<D, 0>(tmem + 256 + 128 * t, tmem + 128 * t, vd, pv & kPvFirst ? 0u : 1u);
+      if (pv & kPvLast) mma_commit(smem_u32(sh.bars + C::kOFull + t));
+      if (pv & kPvCloses) mma_commit(smem_u32(sh.bars + C::kKVEmpty + vst));
+    }
+    __syncwarp();
     return true;
   };
 
   Item x;
-  for (int it = 0; ok && take_item<D, true>(sh, p, it, x, 10); ++it) {
+  for (int it = 0; ok && take_item<D>(sh, p, it, x, 10); ++it) {
     const int tiles = x.ntok > p.tile_tokens ? 2 : 1;
     const int n = x.j1 - x.j0;
     int kst = 0;
@@ -528,17 +610,21 @@ __device__ __forceinline__ void mma_issuer(const Shared& sh, const Params& p, ui
         if ((pv2 & kPvLive) && !issue_pv(pv2)) { ok = false; break; }
         if (s == 0) {
           kst = kv_it % C::kStages;
-          if (!wait_bar(sh, p, C::kKVFull + kst, (kv_it / C::kStages) & 1, 13)) { ok = false; break; }
+          if (!warp_wait(sh, p, C::kKVFull + kst, (kv_it / C::kStages) & 1, 13)) { ok = false; break; }
           ++kv_it;
         }
         const int slot = (q_it + s) & 1;
-        if (j == 0 && !wait_bar(sh, p, C::kQFull + slot, ((q_it + s) >> 1) & 1, 11)) { ok = false; break; }
+        if (j == 0 && !warp_wait(sh, p, C::kQFull + slot, ((q_it + s) >> 1) & 1, 11)) { ok = false; break; }
         tc_fence_after();
-        issue_s_slice<D, 0>(tmem + 128 * t, smem_desc_sw128(smem_u32(q_tile<D>(sh, slot)), 16, 1024),
-                            smem_desc_sw128(smem_u32(kv_tile<D>(sh, kst)), 16, 1024));
-        mma_commit(smem_u32(sh.bars + C::kSFull + t));
-        if (s == tiles - 1) mma_commit(smem_u32(sh.bars + C::kKVEmpty + kst));
-        if (j == n - 1) mma_commit(smem_u32(sh.bars + C::kQEmpty + slot));
+        const uint64_t qd = smem_desc_sw128(smem_u32(q_tile<D>(sh, slot)), 16, 1024);
+        const uint64_t kd = smem_desc_sw128(smem_u32(kv_tile<D>(sh, kst)), 16, 1024);
+        if (elect_one()) {
+          issue_s_slice<D, 0>(tmem + 128 * t, qd, kd);
+          mma_commit(smem_u32(sh.bars + C::kSFull + t));
+          if (s == tiles - 1) mma_commit(smem_u32(sh.bars + C::kKVEmpty + kst));
+          if (j == n - 1) mma_commit(smem_u32(sh.bars + C::kQEmpty + slot));
+        }
+        __syncwarp();
         pv2 = pv1;
         // first and last subtile of its stream in this item
         const int step = tiles == 2 ? 1 : 2;
@@ -554,7 +640,8 @@ __device__ __forceinline__ void mma_issuer(const Shared& sh, const Params& p, ui
     pv1 = 0;
   }
   // all issued MMAs complete before TMEM is released
-  mma_commit(smem_u32(sh.bars + C::kMmaDone));
+  if (elect_one()) mma_commit(smem_u32(sh.bars + C::kMmaDone));
+  __syncwarp();
   const uint32_t addr = smem_u32(sh.bars + C::kMmaDone);
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait(addr, 0) && global_timer_ns() - t0 < p.timeout_ns) {
@@ -595,29 +682,43 @@ __device__ __forceinline__ void softmax_role(const Shared& sh, const Params& p, 
   const uint32_t s_tm = tmem + lane_off + uint32_t(128 * t);
   const uint32_t o_tm = tmem + lane_off + uint32_t(256 + 128 * t);
   const int32_t prefix_len = p.hdr->prefix_len;
-  const int32_t row_tok = row / p.group, row_head = row - row_tok * p.group;
+  const int32_t row_tok = row / p.group;
   uint32_t s_phase = 0, o_phase = 0;
-  Item x;
-  for (int it = 0; take_item<D>(sh, p, it, x, 20 + t); ++it) {
-    const bool pair = x.ntok > p.tile_tokens;
-    const int32_t tile = pair ? t ^ x.parity : 0;               // row tile of this stream
-    const int32_t tok_i = tile * p.tile_tokens + row_tok;        // token inside the unit
-    const bool live = row_tok < p.tile_tokens && tok_i < x.ntok;
-    const bool warp_live = __any_sync(0xffffffffu, live);
-    const int32_t pos = x.pos0 + tok_i;
-    // own keys that this row sees
-    const int64_t seen = (int64_t(pos) / p.block_tokens + 1) * p.block_tokens;
-    const int32_t limit = seen < x.len ? int32_t(seen) : x.len;
-    const int step = pair ? 1 : 2;
+  for (int it = 0;; ++it) {
+    // The item stays in shared memory until its epilogue is done and is read
+    // again there: held in registers across the key tiles it made ptxas spill.
+    if (!warp_wait(sh, p, C::kItemFull + it % kItems, (it / kItems) & 1, 20 + t)) return;
+    const uint32_t item = smem_u32(sh.items + it % kItems);
+    const int32_t j1 = item_field(item, offsetof(Item, j1));
+    if (j1 == 0) return;
+    bool warp_live;
+    int32_t j, step, limit, ptiles;
+    {
+      const int32_t ntok = item_field(item, offsetof(Item, ntok));
+      const bool pair = ntok > p.tile_tokens;
+      const int32_t other = t ^ item_field(item, offsetof(Item, parity));
+      const int32_t tok_i = (pair && other ? p.tile_tokens : 0) + row_tok;  // token inside the unit
+      warp_live = __any_sync(0xffffffffu, row_tok < p.tile_tokens && tok_i < ntok);
+      // own keys that this row sees
+      const int32_t pos = item_field(item, offsetof(Item, pos0)) + tok_i;
+      // (at most pos + block: below 2^32)
+      const uint32_t seen = (uint32_t(pos) / uint32_t(p.block_tokens) + 1) * uint32_t(p.block_tokens);
+      const uint32_t len = uint32_t(item_field(item, offsetof(Item, len)));
+      limit = int32_t(seen < len ? seen : len);
+      ptiles = item_field(item, offsetof(Item, ptiles));
+      // two row tiles: every key tile for one of them; one: every second key tile
+      j = item_field(item, offsetof(Item, j0)) + (pair ? 0 : other);
+      step = pair ? 1 : 2;
+    }
     float m_ref = -INFINITY;  // reference max (log2 units)
     float l = 0.f;
     bool first = true;
-    for (int j = x.j0 + (pair ? 0 : t ^ x.parity); j < x.j1; j += step) {
+    for (; j < j1; j += step) {
       if (!warp_wait(sh, p, C::kSFull + t, s_phase, 22 + t)) return;
       s_phase ^= 1;
       if (warp_live) {
         tc_fence_after();
-        const int32_t visible = j < x.ptiles ? prefix_len - j * 128 : limit - (j - x.ptiles) * 128;
+        const int32_t visible = j < ptiles ? prefix_len - j * 128 : limit - (j - ptiles) * 128;
         float s[128];
         float mxs[8];
 #pragma unroll
@@ -673,21 +774,25 @@ __device__ __forceinline__ void softmax_role(const Shared& sh, const Params& p, 
       mbar_arrive(smem_u32(sh.bars + C::kPFull + t));
     }
     // epilogue
-    const int32_t head = x.head * p.group + row_head;
-    const int32_t tok = x.tok0 + tok_i;
-    const int32_t part = pair ? tile : t;  // row tile or key parity: which half of a partial slot
-    if (first) {
-      // no key tile of this item on this stream: a direct item's row is the other stream's
-      if (!live || x.dest == kDirect) continue;
-    } else {
+    if (!first) {
       if (!warp_wait(sh, p, C::kOFull + t, o_phase, 24 + t)) return;
       o_phase ^= 1;
       tc_fence_after();
     }
-    if (!warp_live) continue;
+    const int32_t ntok = item_field(item, offsetof(Item, ntok)), dest = item_field(item, offsetof(Item, dest));
+    const bool pair = ntok > p.tile_tokens;
+    const int32_t tile = pair ? t ^ item_field(item, offsetof(Item, parity)) : 0;  // row tile of this stream
+    const int32_t tok_i = tile * p.tile_tokens + row_tok;
+    const int32_t head = item_field(item, offsetof(Item, head)) * p.group + (row - row_tok * p.group);
+    const int32_t tok = item_field(item, offsetof(Item, tok0)) + tok_i;
+    const int32_t cbase = item_field(item, offsetof(Item, cbase));
+    release_item<D>(sh, it);
+    // no key tile of this item on this stream: a direct item's rows are the other stream's
+    if (!warp_live || (first && dest == kDirect)) continue;
+    const bool live = row_tok < p.tile_tokens && tok_i < ntok;
     const float inv_l = l > 0.f ? 1.0f / l : 0.f;
     const float lse_row = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
-    if (x.dest == kDirect) {
+    if (dest == kDirect) {
       uint4* dst = reinterpret_cast<uint4*>(p.out + (int64_t(tok) * p.H + head) * D);
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) {
@@ -710,22 +815,17 @@ __device__ __forceinline__ void softmax_role(const Shared& sh, const Params& p, 
       continue;
     }
     // partial row: normalised O and LSE
-    float* po;
-    float* pl;
+    int64_t prow;
     bool store = live;
-    if (x.dest == kMainOwn || x.dest == kMainPrefix) {
-      int32_t ct = x.cbase + tok_i;
-      if (x.dest == kMainPrefix) ct = live ? __ldg(p.ctok + tok) : -1;
+    if (dest == kMainOwn || dest == kMainPrefix) {
+      int32_t ct = cbase + tok_i;
+      if (dest == kMainPrefix) ct = live ? __ldg(p.ctok + tok) : -1;
       store = live && ct >= 0;  // a larger request's row in a shared tile has its prefix elsewhere
-      const int32_t key_half = pair ? 0 : t;
-      const int64_t prow = (int64_t((x.dest == kMainOwn ? 2 : 0) + key_half) * p.max_ctok + (store ? ct : 0)) * p.H + head;
-      po = p.main_o + prow * D;
-      pl = p.main_lse + prow;
+      prow = main_row(p, dest == kMainOwn, pair ? 0 : t, store ? ct : 0, head);
     } else {
-      const int64_t prow = ((int64_t(blockIdx.x) * 2 + (x.dest == kCutTail)) * 2 + part) * 128 + row;
-      po = p.cut_o + prow * D;
-      pl = p.cut_lse + prow;
+      prow = cut_row(p, int(blockIdx.x), dest == kCutTail, pair ? tile : t, row);
     }
+    float* po = p.part_o + prow * D;
     if (!first) {
       float4* dst = reinterpret_cast<float4*>(po);
 #pragma unroll
@@ -741,7 +841,7 @@ __device__ __forceinline__ void softmax_role(const Shared& sh, const Params& p, 
         }
       }
     }
-    if (store) *pl = lse_row;
+    if (store) p.part_lse[prow] = lse_row;
   }
 }
 
@@ -752,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   const Shared sh = carve_smem<D>(smem_raw);
-  const int warp = threadIdx.x / 32;
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) / 32, 0);
   const int lane = threadIdx.x % 32;
 
   if (warp == 9 && lane == 0) {
@@ -785,10 +885,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     softmax_role<D>(sh, p, tmem, warp / 4);
   } else {
     regs_decrease<kControlRegs>();
-    if (warp == 8) {
-      if (lane == 0) mma_issuer<D>(sh, p, tmem);
-      __syncwarp();
-    } else if (warp == 9)
+    if (warp == 8)
+      mma_issuer<D>(sh, p, __shfl_sync(0xffffffffu, tmem, 0));
+    else if (warp == 9)
       producer<D>(sh, p, &tm_q, &tm_k, &tm_v);
     else if (warp == 10)
       scheduler<D>(sh, p);
@@ -804,110 +903,162 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- merging parts
-// One warp per row at a time.  A row's parts, in this order: its own unit's
-// shares, then (rows of small requests) the shares of the prefix unit that
-// holds its token.
-struct Merge {
-  float m, l;
-  float acc[4];
+// One warp per row.  A row's parts, in this order: its own unit's shares, then
+// (rows of small requests) the shares of the prefix unit that holds its token.
+// Up to 32 parts at a time: lane i finds part i's row and LSE, the warp their
+// maximum and weights, and the O rows are then summed four dims per lane, the
+// loads independent of one another.
+struct Parts {
+  int64_t s;      // cost position of the unit
+  int32_t shift, ktiles;
+  int c0, n;      // first share; parts
+  bool pair, cut, own;
+  int32_t half, row;  // of a two-tile unit: the row's tile; the row in its tile
 };
 
-template <int D>
-__device__ __forceinline__ void merge_part(Merge& g, const float* o, const float* lse, int lane) {
-  const float x = *lse;
-  if (x == -INFINITY) return;  // saw no key; its O row is not written
-  constexpr int V = D / 32;
-  float v[V];
-  if constexpr (V == 4) {
-    const float4 f = reinterpret_cast<const float4*>(o)[lane];
-    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-  } else {
-    const float2 f = reinterpret_cast<const float2*>(o)[lane];
-    v[0] = f.x; v[1] = f.y;
-  }
-  const float m = fmaxf(g.m, x);
-  const float a = g.m == -INFINITY ? 0.f : expf(g.m - m), b = expf(x - m);
-  g.l = g.l * a + b;
-#pragma unroll
-  for (int k = 0; k < V; ++k) g.acc[k] = g.acc[k] * a + b * v[k];
-  g.m = m;
+__device__ __forceinline__ Parts parts_of(const Params& p, const Line& line, const wf_batch_unit& u, int64_t s, int32_t tok_i,
+                                          int32_t row_head) {
+  Parts q;
+  q.s = s;
+  q.pair = u.ntok > p.tile_tokens;
+  q.shift = tile_shift(u.ntok, p.tile_tokens);
+  q.ktiles = u.ktiles;
+  q.c0 = share_of(line, s);
+  const int c1 = u.ktiles == 1 ? q.c0 : share_of(line, s + (int64_t(u.ktiles - 1) << q.shift));
+  q.cut = c1 > q.c0;
+  q.own = u.req >= 0;
+  q.n = (c1 - q.c0 + 1) * (q.pair ? 1 : 2);
+  q.half = tok_i >= p.tile_tokens;
+  q.row = (tok_i - q.half * p.tile_tokens) * p.group + row_head;
+  return q;
+}
+
+// Row index of part i, or -1 if that share holds none of the unit's tiles.
+__device__ __forceinline__ int64_t part_row(const Params& p, const Line& line, const Parts& q, int i, int32_t ct, int32_t head) {
+  const int half = q.pair ? q.half : i & 1;
+  if (!q.cut) return main_row(p, q.own, q.pair ? 0 : half, ct, head);
+  const int c = q.c0 + (q.pair ? i : i >> 1);
+  int32_t j0, j1;
+  share_tiles(q.s, q.shift, q.ktiles, share_begin(line, c), share_begin(line, c + 1), j0, j1);
+  return j0 < j1 ? cut_row(p, c, j0 == 0, half, q.row) : -1;
 }
 
 template <int D>
-__device__ __forceinline__ void merge_unit(Merge& g, const Params& p, const wf_batch_unit& u, int64_t s, int64_t total,
-                                           int ctas, int32_t tok_i, int32_t row_head, int32_t ct, int32_t head, int lane) {
-  const bool pair = u.ntok > p.tile_tokens;
-  const int32_t w = tile_cost(u.ntok, p.tile_tokens);
-  const int c0 = share_of(s, total, ctas), c1 = share_of(s + int64_t(u.ktiles - 1) * w, total, ctas);
-  if (c0 == c1) {
-    const int64_t prow = (int64_t(u.req < 0 ? 0 : 2) * p.max_ctok + ct) * p.H + head;
-    merge_part<D>(g, p.main_o + prow * D, p.main_lse + prow, lane);
-    if (!pair) {
-      const int64_t odd = prow + int64_t(p.max_ctok) * p.H;
-      merge_part<D>(g, p.main_o + odd * D, p.main_lse + odd, lane);
+__device__ __forceinline__ void merge_row(const Params& p, const Line& line, const Parts& a, const Parts& b, int32_t ct,
+                                          int32_t tok, int32_t head) {
+  constexpr int V = D / 32;  // dims per lane
+  const int lane = threadIdx.x & 31;
+  float m = -INFINITY, l = 0.f;
+  float acc[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) acc[k] = 0.f;
+  const int n = a.n + b.n;
+  for (int base = 0; base < n; base += 32) {
+    const int i = base + lane;
+    int64_t row = -1;
+    if (i < a.n)
+      row = part_row(p, line, a, i, ct, head);
+    else if (i < n)
+      row = part_row(p, line, b, i - a.n, ct, head);
+    const float x = row >= 0 ? p.part_lse[row] : -INFINITY;
+    float mx = x;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    if (mx == -INFINITY) continue;
+    const float m_new = fmaxf(m, mx);
+    const float old = m == -INFINITY ? 0.f : expf(m - m_new);
+    const float w = x == -INFINITY ? 0.f : expf(x - m_new);
+    float ws = w;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, off);
+    l = l * old + ws;
+    m = m_new;
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] *= old;
+    // a part that saw no key has no O row
+    uint32_t todo = __ballot_sync(0xffffffffu, x != -INFINITY);
+    while (todo) {
+      float o[4][V], wk[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int src = todo ? __ffs(todo) - 1 : 0;
+        const bool any = todo != 0;
+        todo &= todo - 1;
+        wk[k] = any ? __shfl_sync(0xffffffffu, w, src) : 0.f;
+        const int64_t r = __shfl_sync(0xffffffffu, row, src);
+        if (any) {
+          if constexpr (V == 4) {
+            const float4 f = reinterpret_cast<const float4*>(p.part_o + r * D)[lane];
+            o[k][0] = f.x; o[k][1] = f.y; o[k][2] = f.z; o[k][3] = f.w;
+          } else {
+            const float2 f = reinterpret_cast<const float2*>(p.part_o + r * D)[lane];
+            o[k][0] = f.x; o[k][1] = f.y;
+          }
+        } else {
+#pragma unroll
+          for (int v = 0; v < V; ++v) o[k][v] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = fmaf(wk[k], o[k][v], acc[v]);
     }
-    return;
   }
-  const int32_t tile = tok_i / p.tile_tokens;
-  const int32_t row = (tok_i - tile * p.tile_tokens) * p.group + row_head;
-  for (int c = c0; c <= c1; ++c) {
-    int32_t j0, j1;
-    share_tiles(s, w, u.ktiles, share_begin(c, total, ctas), share_begin(c + 1, total, ctas), j0, j1);
-    if (j0 >= j1) continue;
-    const int64_t slot = (int64_t(c) * 2 + (j0 == 0)) * 2;
-    for (int k = pair ? tile : 0; k <= (pair ? tile : 1); ++k) {
-      const int64_t prow = (slot + k) * 128 + row;
-      merge_part<D>(g, p.cut_o + prow * D, p.cut_lse + prow, lane);
-    }
+  const float inv = l > 0.f ? 1.0f / l : 0.f;
+  __nv_bfloat16* dst = p.out + (int64_t(tok) * p.H + head) * D;
+  if constexpr (V == 4) {
+    uint2 o;
+    o.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    o.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
+    reinterpret_cast<uint2*>(dst)[lane] = o;
+  } else {
+    reinterpret_cast<uint32_t*>(dst)[lane] = pack_bf16x2(acc[0] * inv, acc[1] * inv);
   }
+  if (lane == 0 && p.lse) p.lse[int64_t(head) * p.max_tokens + tok] = l > 0.f ? m + logf(l) : -INFINITY;
 }
 
 constexpr int kCombineThreads = 256;
+constexpr int kCombineWarps = kCombineThreads / 32;
 
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads) batch_combine_kernel(const Params p) {
   const wf_batch_hdr* h = p.hdr;
-  const int64_t head_cost = h->head_cost, total = head_cost * p.kv_heads;
-  if (h->fingerprint != p.fingerprint || total == 0) return;
-  const int lane = threadIdx.x & 31;
-  const int ctas = h->ctas, np = h->prefix_units, own = h->units - np;
-  const int subs = h->max_rows < 32 ? h->max_rows : 32;  // warps that share a unit's rows
-  const int64_t tasks = int64_t(own) * p.kv_heads * subs;
-  const int64_t warps = int64_t(gridDim.x) * (kCombineThreads / 32);
-  for (int64_t k = int64_t(blockIdx.x) * (kCombineThreads / 32) + (threadIdx.x >> 5); k < tasks; k += warps) {
-    const int32_t sub = int32_t(k % subs), kv = int32_t(k / subs % p.kv_heads), ui = np + int32_t(k / subs / p.kv_heads);
-    const wf_batch_unit u = p.units[ui];
-    const int64_t s = int64_t(kv) * head_cost + p.pre[ui];
-    if (unit_direct(u, p.tile_tokens)) {
-      const int64_t last = s + int64_t(u.ktiles - 1) * tile_cost(u.ntok, p.tile_tokens);
-      if (share_of(s, total, ctas) == share_of(last, total, ctas)) continue;  // written by the attention
-    }
-    for (int32_t r = sub; r < u.ntok * p.group; r += subs) {
-      const int32_t tok_i = r / p.group, row_head = r - tok_i * p.group;
-      const int32_t tok = u.tok0 + tok_i, head = kv * p.group + row_head;
-      Merge g;
-      g.m = -INFINITY;
-      g.l = 0.f;
-      for (int x = 0; x < 4; ++x) g.acc[x] = 0.f;
-      const int32_t ct = u.cbase + tok_i;
-      merge_unit<D>(g, p, u, s, total, ctas, tok_i, row_head, ct, head, lane);
-      if (u.ptiles < 0) {
-        const int32_t pu = tok / (2 * p.tile_tokens);
-        const wf_batch_unit q = p.units[pu];
-        merge_unit<D>(g, p, q, int64_t(kv) * head_cost + p.pre[pu], total, ctas, tok - q.tok0, row_head, ct, head, lane);
-      }
-      const float inv = g.l > 0.f ? 1.0f / g.l : 0.f;
-      __nv_bfloat16* dst = p.out + (int64_t(tok) * p.H + head) * D;
-      if constexpr (D == 128) {
-        uint2 o;
-        o.x = pack_bf16x2(g.acc[0] * inv, g.acc[1] * inv);
-        o.y = pack_bf16x2(g.acc[2] * inv, g.acc[3] * inv);
-        reinterpret_cast<uint2*>(dst)[lane] = o;
-      } else {
-        reinterpret_cast<uint32_t*>(dst)[lane] = pack_bf16x2(g.acc[0] * inv, g.acc[1] * inv);
-      }
-      if (lane == 0 && p.lse) p.lse[int64_t(head) * p.max_tokens + tok] = g.l > 0.f ? g.m + logf(g.l) : -INFINITY;
-    }
+  const Line line = line_of(p);
+  if (h->fingerprint != p.fingerprint || line.total == 0) return;
+  const int warp = threadIdx.x >> 5;
+  const int np = h->prefix_units;
+  Parts none{};
+  // rows of one-tile units, a warp each
+  const int64_t rows = int64_t(h->ctoks) * p.H;
+  for (int64_t k = int64_t(blockIdx.x) * kCombineWarps + warp; k < rows; k += int64_t(gridDim.x) * kCombineWarps) {
+    const int32_t ct = int32_t(uint32_t(k) / uint32_t(p.H)), head = int32_t(uint32_t(k) - uint32_t(ct) * uint32_t(p.H));
+    const wf_batch_ctok at = p.ctok_list[ct];
+    const int32_t pu = at.tok / (2 * p.tile_tokens);
+    const wf_batch_unit u = p.units[at.unit], q = p.units[pu < np ? pu : at.unit];
+    const int64_t pre_u = p.pre[at.unit], pre_q = p.pre[pu < np ? pu : at.unit];
+    if (unit_direct(u, p.tile_tokens)) continue;  // a single tile, never cut
+    const int32_t kv = head / p.group, row_head = head - kv * p.group;
+    const int64_t s0 = int64_t(kv) * line.head_cost;
+    const Parts a = parts_of(p, line, u, s0 + pre_u, at.tok - u.tok0, row_head);
+    const Parts b = u.ptiles < 0 ? parts_of(p, line, q, s0 + pre_q, at.tok - q.tok0, row_head) : none;
+    merge_row<D>(p, line, a, b, ct, at.tok, head);
+  }
+  // rows of two-tile units that were cut, a block for 8 rows; a unit is taken up at its first cut
+  if (p.max_tokens <= p.tile_tokens) return;
+  constexpr int kGroups = 256 / kCombineWarps;
+  for (int k = blockIdx.x; k < h->ctas * kGroups; k += gridDim.x) {
+    const int c = k / kGroups, r = k % kGroups * kCombineWarps + warp;
+    const int2 cut = p.cuts[c];
+    // (out of range only where a CTA gave up before it noted its cut)
+    if (cut.y < 0 || cut.y >= h->units || cut.x < 0 || cut.x >= p.kv_heads) continue;
+    const wf_batch_unit u = p.units[cut.y];
+    if (u.req < 0 || u.ntok <= p.tile_tokens || r >= u.ntok * p.group) continue;
+    const int32_t tok_i = r / p.group, row_head = r - tok_i * p.group;
+    const Parts a = parts_of(p, line, u, int64_t(cut.x) * line.head_cost + p.pre[cut.y], tok_i, row_head);
+    bool first = true;
+    for (int d = a.c0 + 1; d < c; ++d) first &= p.cuts[d].y < 0;
+    if (first) merge_row<D>(p, line, a, none, 0, u.tok0 + tok_i, cut.x * p.group + row_head);
   }
 }
 
@@ -964,8 +1115,8 @@ wf_status launch(const wf_batch_desc* d, const BatchLayout& L, const Params& p, 
     return WF_ERR_CUDA;
   batch_attn_kernel<D><<<L.ctas, kThreads, Cfg<D>::kSmemBytes, stream>>>(tq, tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return WF_ERR_CUDA;
-  // as many warps as rows at most
-  const int64_t rows = int64_t(d->max_tokens) * d->num_heads;
+  // a warp per row that can need merging, as long as they run at once
+  const int64_t rows = int64_t(L.max_ctok) * d->num_heads + (d->max_tokens > L.tile_tokens ? int64_t(L.ctas) * 256 : 0);
   const int64_t blocks = (rows + kCombineThreads / 32 - 1) / (kCombineThreads / 32);
   const int64_t most = int64_t(L.ctas) * 8;
   batch_combine_kernel<D><<<unsigned(blocks < most ? blocks : most), kCombineThreads, 0, stream>>>(p);
@@ -1008,15 +1159,16 @@ extern "C" wf_status wf_batch_attn(const wf_batch_desc* desc, const void* plan, 
   p.units = reinterpret_cast<const wf_batch_unit*>(pl + L.off_units);
   p.pre = reinterpret_cast<const int64_t*>(pl + L.off_pre);
   p.ctok = reinterpret_cast<const int32_t*>(pl + L.off_ctok);
+  p.ctok_list = reinterpret_cast<const wf_batch_ctok*>(pl + L.off_ctok_list);
   p.table = block_table;
   p.prefix_table = prefix_table;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   p.status = reinterpret_cast<wf_dev_status*>(ws);
-  p.main_o = reinterpret_cast<float*>(ws + WF_ATTN_STATUS_BYTES);
-  p.cut_o = reinterpret_cast<float*>(ws + L.off_cut_o);
-  p.main_lse = reinterpret_cast<float*>(ws + L.off_main_lse);
-  p.cut_lse = reinterpret_cast<float*>(ws + L.off_cut_lse);
+  p.part_o = reinterpret_cast<float*>(ws + WF_ATTN_STATUS_BYTES);
+  p.part_lse = reinterpret_cast<float*>(ws + L.off_lse);
+  p.cuts = reinterpret_cast<int2*>(ws + L.off_cuts);
+  p.main_rows = L.main_rows;
   p.fingerprint = L.fingerprint;
   p.timeout_ns = wf::wait_timeout_ns();
   p.scale_log2 = float(scale * 1.4426950408889634);

@@ -47,6 +47,7 @@ struct TablesParams {
   wf_batch_unit* units;
   int64_t* pre;    // exclusive sums of unit costs
   int32_t* ctok;   // partial-row index of each token, -1 for none
+  wf_batch_ctok* ctok_list;  // and the tokens by that index
   int32_t B, max_tokens, cols, max_prefix, num_free, pool_pages;
   int32_t page, page_shift, group, tile_tokens, block_tokens, kv_heads, max_ctas;
   uint64_t fingerprint;
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesPara
         wf_batch_hdr h{};
         h.status.code = (bad & 1) ? WF_ERR_INVALID_ARG : WF_ERR_CAPACITY;
         h.fingerprint = p.fingerprint;
-        h.ctas = 1;
+        h.share = 1;
         *p.hdr = h;
         p.pre[0] = 0;
       }
@@ -188,6 +189,8 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesPara
   }
   __syncthreads();
 
+  const int32_t pair_tokens = 2 * Tt;
+  const int32_t np = shared ? (tokens + pair_tokens - 1) / pair_tokens : 0;  // prefix units
   if (blockIdx.x > 0) {
     for (int64_t t64 = int64_t(blockIdx.x - 1) * kThreads + tid; t64 < tokens; t64 += int64_t(gridDim.x - 1) * kThreads) {
       const int32_t t = int32_t(t64);
@@ -207,15 +210,15 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesPara
       p.slot_map[t] = pg >= 0 && pg < p.pool_pages ? pg * p.page + in_page : -1;
       p.positions[t] = prefix + x;
       const int32_t tiles = (f + Tt - 1) / Tt, tail = (tiles - 1) * Tt;
-      p.ctok[t] = (tiles & 1) && i >= tail ? s_ctok[b] + i - tail : -1;
+      const int32_t ct = (tiles & 1) && i >= tail ? s_ctok[b] + i - tail : -1;
+      p.ctok[t] = ct;
+      if (ct >= 0) p.ctok_list[ct] = {t, np + s_unit[b + 1] - 1};
     }
     return;
   }
 
   // ---- block 0: the attention's units and the running sum of their costs
   const int32_t ptiles = (prefix + 127) >> 7;
-  const int32_t pair_tokens = 2 * Tt;
-  const int32_t np = shared ? (tokens + pair_tokens - 1) / pair_tokens : 0;
   const int32_t own = s_unit[p.B];
   for (int u = tid; u < np; u += kThreads) {
     wf_batch_unit r;
@@ -256,25 +259,18 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesPara
     }
   __syncthreads();
   int64_t carry = 0;
-  int32_t rows = 0;
   for (int u0 = 0; u0 < np + own; u0 += kThreads) {
     const int u = u0 + tid;
     int64_t cost[1] = {0}, sum[1];
     if (u < np + own) {
       const int32_t kt = p.units[u].ktiles, nt = p.units[u].ntok;
-      cost[0] = kt == 0 ? 0 : int64_t(kt) * (nt > Tt ? WF_BATCH_PAIR_COST : WF_BATCH_SINGLE_COST) + WF_BATCH_UNIT_COST;
-      rows = max(rows, nt * p.group);
+      if (kt > 0)
+        cost[0] = (int64_t(kt) << (nt > Tt ? WF_BATCH_PAIR_SHIFT : WF_BATCH_SINGLE_SHIFT)) + WF_BATCH_UNIT_COST;
     }
     block_scan<1>(cost, sum, scratch);
     if (u < np + own) p.pre[u] = carry + cost[0];
     carry += sum[0];
   }
-  for (int off = 16; off > 0; off >>= 1) rows = max(rows, __shfl_xor_sync(0xffffffffu, rows, off));
-  __shared__ int32_t s_rows;
-  if (tid == 0) s_rows = 0;
-  __syncthreads();
-  if ((tid & 31) == 0) atomicMax(&s_rows, rows);
-  __syncthreads();
   if (tid == 0) {
     p.pre[np + own] = carry;
     wf_batch_hdr h{};
@@ -283,11 +279,13 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesPara
     h.units = np + own;
     h.prefix_units = np;
     h.prefix_len = prefix;
-    h.max_rows = s_rows;
+    h.ctoks = int32_t(total[2]);
     h.head_cost = carry;
-    // no CTA gets less than two single tiles: shorter shares cost more in merging than they save
-    const int64_t shares = carry * p.kv_heads / (2 * WF_BATCH_SINGLE_COST);
-    h.ctas = int32_t(max(int64_t(1), min(int64_t(p.max_ctas), shares)));
+    // no share is smaller than two single tiles: shorter ones cost more in merging than they save
+    const int64_t all = carry * p.kv_heads;
+    h.share = max((all + p.max_ctas - 1) / p.max_ctas, int64_t(2) << WF_BATCH_SINGLE_SHIFT);
+    h.share_inv = ~uint64_t(0) / uint64_t(h.share);
+    h.ctas = int32_t((all + h.share - 1) / h.share);
     *p.hdr = h;
   }
 }
@@ -312,7 +310,8 @@ BatchLayout batch_layout(const wf_batch_desc* d) {
   // the work list's 64-bit cost arithmetic, int32 token and page indices
   const int64_t kMaxKeys = int64_t(1) << 27;
   if (K > 256 || H > 4096 || d->max_requests > 8192 || d->max_tokens > (1 << 22) || d->num_ctas > 256 ||
-      d->pool_pages * P > 0x7FFFFFFF || d->max_request_pages * P > kMaxKeys || d->max_prefix_pages * P > kMaxKeys)
+      d->pool_pages * P > 0x7FFFFFFF || int64_t(d->max_requests) * d->max_request_pages > 0x7FFFFFFF ||
+      d->max_request_pages * P > kMaxKeys || d->max_prefix_pages * P > kMaxKeys)
     return L;
   L.ctas = d->num_ctas;
   if (L.ctas == 0) {
@@ -336,14 +335,14 @@ BatchLayout batch_layout(const wf_batch_desc* d) {
   L.off_units = sizeof(wf_batch_hdr);
   L.off_pre = up(L.off_units + size_t(L.max_units) * sizeof(wf_batch_unit));
   L.off_ctok = up(L.off_pre + size_t(L.max_units + 1) * sizeof(int64_t));
-  L.plan_bytes = up(L.off_ctok + size_t(d->max_tokens) * sizeof(int32_t));
-  // partial rows: [prefix, own][key parity][ctok][H] and [ctas][head, tail][tile or key parity][128]
-  const size_t main_rows = size_t(4) * size_t(L.max_ctok) * size_t(H), cut_rows = size_t(L.ctas) * 4 * 128;
-  const size_t row = size_t(d->head_dim) * sizeof(float);
-  L.off_cut_o = up(WF_ATTN_STATUS_BYTES + main_rows * row);
-  L.off_main_lse = up(L.off_cut_o + cut_rows * row);
-  L.off_cut_lse = up(L.off_main_lse + main_rows * sizeof(float));
-  L.workspace_bytes = up(L.off_cut_lse + cut_rows * sizeof(float));
+  L.off_ctok_list = up(L.off_ctok + size_t(d->max_tokens) * sizeof(int32_t));
+  L.plan_bytes = up(L.off_ctok_list + size_t(L.max_ctok) * sizeof(wf_batch_ctok));
+  // partial rows: [prefix, own][key parity][ctok][H], then [ctas][head, tail][tile or key parity][128]
+  L.main_rows = 4 * L.max_ctok * H;
+  const size_t rows = size_t(L.main_rows) + size_t(L.ctas) * 4 * 128;
+  L.off_lse = up(WF_ATTN_STATUS_BYTES + rows * size_t(d->head_dim) * sizeof(float));
+  L.off_cuts = up(L.off_lse + rows * sizeof(float));
+  L.workspace_bytes = up(L.off_cuts + size_t(L.ctas) * 2 * sizeof(int32_t));
   uint64_t f = 0xcbf29ce484222325ull;  // FNV-1a over the description's words
   const int32_t words[] = {d->num_heads, d->num_kv_heads, d->head_dim, d->dtype, d->page_tokens, d->pool_pages,
                            d->max_requests, d->max_tokens, d->max_request_pages, d->max_prefix_pages,
@@ -410,6 +409,7 @@ extern "C" wf_status wf_batch_tables(const wf_batch_desc* desc, const int32_t* c
   p.units = reinterpret_cast<wf_batch_unit*>(pl + L.off_units);
   p.pre = reinterpret_cast<int64_t*>(pl + L.off_pre);
   p.ctok = reinterpret_cast<int32_t*>(pl + L.off_ctok);
+  p.ctok_list = reinterpret_cast<wf_batch_ctok*>(pl + L.off_ctok_list);
   p.B = desc->max_requests;
   p.max_tokens = desc->max_tokens;
   p.cols = desc->max_request_pages;

@@ -11,10 +11,11 @@
 #include "wf_plan.h"
 
 // Key tiles are shared out to CTAs by cost.  A tile against two row tiles
-// (256 rows) costs WF_BATCH_PAIR_COST, against one WF_BATCH_SINGLE_COST, and
-// every unit WF_BATCH_UNIT_COST more for filling and draining the pipeline.
-#define WF_BATCH_PAIR_COST 8
-#define WF_BATCH_SINGLE_COST 4
+// (256 rows) costs 1 << WF_BATCH_PAIR_SHIFT, against one 1 <<
+// WF_BATCH_SINGLE_SHIFT, and every unit WF_BATCH_UNIT_COST more for filling
+// and draining the pipeline.
+#define WF_BATCH_PAIR_SHIFT 3
+#define WF_BATCH_SINGLE_SHIFT 2
 #define WF_BATCH_UNIT_COST 4
 
 // One work unit of the attention, for one key head: up to two 128-row tiles of
@@ -39,10 +40,17 @@ struct wf_batch_hdr {
   int32_t units;          // 28: records in the unit list
   int32_t prefix_units;   // 32: of them, the leading ones with req = -1
   int32_t prefix_len;     // 36
-  int32_t ctas;           // 40: CTAs that the work is shared out to
-  int32_t max_rows;       // 44: most query rows (tokens x group) of any unit
+  int32_t ctas;           // 40: CTAs that get a share
+  int32_t ctoks;          // 44: tokens of one-tile units
   int64_t head_cost;      // 48: cost of one key head's units
-  int32_t pad[50];
+  int64_t share;          // 56: cost of a CTA's share of all heads'
+  uint64_t share_inv;     // 64: floor((2^64 - 1) / share)
+  int32_t pad[46];
+};
+
+// A token of a one-tile unit: its rows may have to be merged from parts.
+struct wf_batch_ctok {
+  int32_t tok, unit;
 };
 static_assert(sizeof(wf_batch_hdr) == 256, "batch plan header layout");
 
@@ -56,8 +64,9 @@ struct BatchLayout {
   int32_t ctas;
   int32_t max_units;
   int64_t max_ctok;      // capacity of partial-row tokens
-  size_t off_units, off_pre, off_ctok, plan_bytes;
-  size_t off_cut_o, off_main_lse, off_cut_lse, workspace_bytes;  // partial O first, after the status block
+  size_t off_units, off_pre, off_ctok, off_ctok_list, plan_bytes;
+  int64_t main_rows;     // partial rows of uncut units; those of the CTAs' cuts follow
+  size_t off_cuts, off_lse, workspace_bytes;  // partial O first, after the status block
   uint64_t fingerprint;
 };
 

@@ -246,7 +246,6 @@ def wf_attn_noalloc_status(stream=None):
     return code, list(detail)
 
 
-
 def wf_quantize_fp8(host_plan, src, dst8, scales, which, stream=None):
     _check(lib().wf_quantize_fp8(_ptr(host_plan), _ptr(src), _ptr(dst8), _ptr(scales), int(which), _stream(stream)),
            "wf_quantize_fp8")
@@ -268,30 +267,31 @@ def wf_batch_workspace_bytes(desc: BatchDesc) -> int:
     return lib().wf_batch_workspace_bytes(ctypes.byref(desc))
 
 
-def _room(where, *args):
-    """(tensor, elements, element size): raises where a tensor is not dense or too small for what the call may touch.
-    Raw addresses and None pass: their owner vouches for them."""
-    for x, n, size in args:
-        if x is not None and not isinstance(x, (int, np.ndarray)) and (
-                not x.is_contiguous() or x.element_size() != size or x.numel() < n):
-            raise WfError(WF_ERR_INVALID_ARG, f"{where}: a tensor of {x.numel()} x {x.element_size()} bytes "
-                                              f"(contiguous: {x.is_contiguous()}) where {n} x {size} are needed")
+def _room(where, x, n, size):
+    """Address of x, which must be dense and hold n elements of `size` bytes.  Raw addresses and None pass as they are:
+    their owner vouches for them."""
+    if x is None or type(x) is int:
+        return x
+    if isinstance(x, np.ndarray):
+        return x.ctypes.data
+    if x.is_contiguous() and x.itemsize == size and x.numel() >= n:
+        return x.data_ptr()
+    raise WfError(WF_ERR_INVALID_ARG, f"{where}: {x.numel()} elements of {x.itemsize} bytes (dense: "
+                                      f"{x.is_contiguous()}) where {n} of {size} are needed")
 
 
 def wf_batch_tables(desc: BatchDesc, cached, fresh, prefix_len, free_pages, free_head, free_head_out, block_table,
                     token_start, slot_map, positions, plan, held=None, held_out=None, stream=None, num_free=None,
                     plan_bytes=None):
-    B = desc.max_requests
-    _room("wf_batch_tables", (cached, B, 4), (fresh, B, 4), (prefix_len, 1, 4), (free_pages, num_free or 0, 4),
-          (free_head, 1, 4), (free_head_out, 1, 4), (block_table, B * desc.max_request_pages, 4),
-          (token_start, B + 1, 4), (slot_map, desc.max_tokens, 4), (positions, desc.max_tokens, 4), (held, B, 4),
-          (held_out, B, 4))
+    w, B, T = "wf_batch_tables", desc.max_requests, desc.max_tokens
     nf = num_free if num_free is not None else free_pages.numel()
     pb = plan_bytes if plan_bytes is not None else _nbytes(plan)
-    _check(lib().wf_batch_tables(ctypes.byref(desc), _ptr(cached), _ptr(fresh), _ptr(prefix_len), _ptr(held),
-                                 _ptr(free_pages), nf, _ptr(free_head), _ptr(free_head_out), _ptr(held_out),
-                                 _ptr(block_table), _ptr(token_start), _ptr(slot_map), _ptr(positions), _ptr(plan), pb,
-                                 _stream(stream)), "wf_batch_tables")
+    _check(lib().wf_batch_tables(
+        ctypes.byref(desc), _room(w, cached, B, 4), _room(w, fresh, B, 4), _room(w, prefix_len, 1, 4),
+        _room(w, held, B, 4), _room(w, free_pages, nf, 4), nf, _room(w, free_head, 1, 4),
+        _room(w, free_head_out, 1, 4), _room(w, held_out, B, 4), _room(w, block_table, B * desc.max_request_pages, 4),
+        _room(w, token_start, B + 1, 4), _room(w, slot_map, T, 4), _room(w, positions, T, 4), _ptr(plan), pb,
+        _stream(stream)), w)
 
 
 def wf_batch_status(plan, stream=None):
@@ -300,27 +300,25 @@ def wf_batch_status(plan, stream=None):
 
 
 def wf_batch_append(desc: BatchDesc, plan, slot_map, k, v, k_pool, v_pool, q=None, rope=None, q_rot=None, stream=None):
-    D, pool = desc.head_dim, desc.pool_pages * desc.page_tokens * desc.num_kv_heads * desc.head_dim
     # the step may hold fewer tokens than max_tokens: only the device knows, so room for all is asked for
-    T = desc.max_tokens
-    _room("wf_batch_append", (slot_map, T, 4), (rope, T * D, 4), (q, T * desc.num_heads * D, 2),
-          (q_rot, T * desc.num_heads * D, 2), (k, T * desc.num_kv_heads * D, 2), (v, T * desc.num_kv_heads * D, 2),
-          (k_pool, pool, 2), (v_pool, pool, 2))
-    _check(lib().wf_batch_append(ctypes.byref(desc), _ptr(plan), _ptr(slot_map), _ptr(rope), _ptr(q), _ptr(k), _ptr(v),
-                                 _ptr(q_rot), _ptr(k_pool), _ptr(v_pool), _stream(stream)), "wf_batch_append")
+    w, T, kv_row = "wf_batch_append", desc.max_tokens, desc.num_kv_heads * desc.head_dim
+    pool, q_size = desc.pool_pages * desc.page_tokens * kv_row, T * desc.num_heads * desc.head_dim
+    _check(lib().wf_batch_append(
+        ctypes.byref(desc), _ptr(plan), _room(w, slot_map, T, 4), _room(w, rope, T * desc.head_dim, 4),
+        _room(w, q, q_size, 2), _room(w, k, T * kv_row, 2), _room(w, v, T * kv_row, 2), _room(w, q_rot, q_size, 2),
+        _room(w, k_pool, pool, 2), _room(w, v_pool, pool, 2), _stream(stream)), w)
 
 
 def wf_batch_attn(desc: BatchDesc, plan, block_table, prefix_table, q, k_pool, v_pool, out, lse=None,
                   softmax_scale=0.0, workspace=None, stream=None, workspace_bytes=None):
-    D, pool = desc.head_dim, desc.pool_pages * desc.page_tokens * desc.num_kv_heads * desc.head_dim
-    T, H = desc.max_tokens, desc.num_heads
-    _room("wf_batch_attn", (block_table, desc.max_requests * desc.max_request_pages, 4),
-          (prefix_table, desc.max_prefix_pages, 4), (q, T * H * D, 2), (k_pool, pool, 2), (v_pool, pool, 2),
-          (out, T * H * D, 2), (lse, T * H, 4))
+    w, T, H = "wf_batch_attn", desc.max_tokens, desc.num_heads
+    q_size, pool = T * H * desc.head_dim, desc.pool_pages * desc.page_tokens * desc.num_kv_heads * desc.head_dim
     wb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
-    _check(lib().wf_batch_attn(ctypes.byref(desc), _ptr(plan), _ptr(block_table), _ptr(prefix_table), _ptr(q),
-                               _ptr(k_pool), _ptr(v_pool), _ptr(out), _ptr(lse), float(softmax_scale),
-                               _ptr(workspace), wb, _stream(stream)), "wf_batch_attn")
+    _check(lib().wf_batch_attn(
+        ctypes.byref(desc), _ptr(plan), _room(w, block_table, desc.max_requests * desc.max_request_pages, 4),
+        _room(w, prefix_table, desc.max_prefix_pages, 4), _room(w, q, q_size, 2), _room(w, k_pool, pool, 2),
+        _room(w, v_pool, pool, 2), _room(w, out, q_size, 2), _room(w, lse, T * H, 4), softmax_scale, _ptr(workspace),
+        wb, _stream(stream)), w)
 
 
 def wf_synth_fill(dst, dtype, seed, tensor, tag, n_first, nchunks, C, H, D, kscale=False, stream=None):

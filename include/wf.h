@@ -389,7 +389,8 @@ typedef struct wf_batch_desc {
   int32_t pool_pages;        /* pages of the pool, pool_pages * P < 2^31 */
   int32_t max_requests;      /* B in [1, 8192]; requests without new tokens are fine */
   int32_t max_tokens;        /* most new tokens of a step, in [1, 2^22] */
-  int32_t max_request_pages; /* columns of the block table, at most 2^27 tokens */
+  int32_t max_request_pages; /* columns of the block table, at most 2^27 tokens;
+                                the table has less than 2^31 entries */
   int32_t max_prefix_pages;  /* entries of the prefix table, at most 2^27 tokens; 0: no prefix */
   int32_t block_tokens;      /* G >= 1: see wf_batch_attn */
   int32_t num_ctas;          /* CTAs of the attention, at most 256; 0 = SM count of the
