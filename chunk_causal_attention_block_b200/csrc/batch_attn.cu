@@ -371,9 +371,8 @@ __device__ __forceinline__ void scheduler(const Shared& sh, const Params& p) {
 // the tile's i-th page (16 at most): read from the table once, a tile ahead of
 // its use, for K and V both.
 struct KeyTile {
-  int32_t head;
-  int32_t valid;   // keys, at most 128
-  int32_t at;      // of this lane's page
+  int32_t head_valid;  // key head << 8 | keys (at most 128)
+  int32_t at;          // of this lane's page
 };
 
 __device__ __forceinline__ int32_t tile_keys(const Item& x, int32_t j, int32_t prefix_len) {
@@ -383,14 +382,14 @@ __device__ __forceinline__ int32_t tile_keys(const Item& x, int32_t j, int32_t p
 
 __device__ __forceinline__ KeyTile key_tile(const Params& p, const Item& x, int32_t j, int32_t prefix_len) {
   KeyTile k;
-  k.head = x.head;
-  k.valid = tile_keys(x, j, prefix_len);
+  const int32_t valid = tile_keys(x, j, prefix_len);
+  k.head_valid = x.head << 8 | valid;
   const bool own = j >= x.ptiles;
   const int32_t pg = int32_t(threadIdx.x & 31);
   const int32_t* list = own ? p.table + x.req * p.cols : p.prefix_table;
   const int32_t first = ((own ? j - x.ptiles : j) * 128) >> p.page_shift;
   k.at = 0;
-  if (pg << p.page_shift < k.valid) {
+  if (pg << p.page_shift < valid) {
     // an entry outside the pool reads zeros, not memory: the map's bounds hold
     const int64_t tok = int64_t(__ldg(list + first + pg)) << p.page_shift;
     k.at = tok < 0 || tok > 0x7FFFFF00 ? 0x7FFFFF00 : int32_t(tok);
@@ -404,7 +403,8 @@ __device__ __forceinline__ KeyTile key_tile(const Params& p, const Item& x, int3
 template <int D>
 __device__ __forceinline__ void load_tile(const Shared& sh, const Params& p, const CUtensorMap* tm, const KeyTile& k,
                                           int st, int bar_index) {
-  const int pages = (k.valid + (1 << p.page_shift) - 1) >> p.page_shift;
+  const int head = k.head_valid >> 8, valid = k.head_valid & 255;
+  const int pages = (valid + (1 << p.page_shift) - 1) >> p.page_shift;
   const uint32_t page_bytes = 128u << p.page_shift;  // of one half
   const uint32_t bar = smem_u32(sh.bars + bar_index);
   uint32_t dst = smem_u32(kv_tile<D>(sh, st));
@@ -412,8 +412,8 @@ __device__ __forceinline__ void load_tile(const Shared& sh, const Params& p, con
   for (int pg = 0; pg < pages; ++pg, dst += page_bytes) {
     const int32_t at = __shfl_sync(0xffffffffu, k.at, pg);
     if (elect_one()) {
-      tma_load_3d(dst, tm, bar, 0, k.head, at);
-      if (Cfg<D>::kHalves == 2) tma_load_3d(dst + kHalfBytes, tm, bar, 64, k.head, at);
+      tma_load_3d(dst, tm, bar, 0, head, at);
+      if (Cfg<D>::kHalves == 2) tma_load_3d(dst + kHalfBytes, tm, bar, 64, head, at);
     }
   }
 }
@@ -429,58 +429,67 @@ __device__ __forceinline__ void producer(const Shared& sh, const Params& p, cons
   const int32_t prefix_len = p.hdr->prefix_len;
   int kv_it = 0, q_it = 0;
   uint32_t raw_phase = 0, raw_last = 0;  // per stage: parity of the next raw fill; last fill was raw
-  bool ok = true;
-  KeyTile v1{}, v2{};                    // V tiles of the last and the second last subtile
+  KeyTile cur{}, next{}, v1{}, v2{};     // v1, v2: V tiles of the last and the second last subtile
   bool has1 = false, has2 = false;
   const uint32_t q_bytes = uint32_t(p.tile_tokens * p.group) * 128 * C::kHalves;
 
-  auto fill = [&](const CUtensorMap* tm, const KeyTile& k, bool is_v) -> bool {
-    const int st = kv_it % C::kStages;
-    if (!warp_wait(sh, p, C::kKVEmpty + st, ((kv_it / C::kStages) & 1) ^ 1, 2)) return false;
-    const bool raw = is_v && k.valid < 128;
-    load_tile<D>(sh, p, tm, k, st, raw ? C::kVRaw + st : C::kKVFull + st);
-    raw_last = raw ? raw_last | (1u << st) : raw_last & ~(1u << st);
-    if (raw) raw_phase ^= 1u << st;
-    ++kv_it;
-    return true;
-  };
-
-  int it = 0;
-  Item x;
-  for (; ok && take_item<D>(sh, p, it, x, 1); ++it) {
-    KeyTile next = key_tile(p, x, x.j0, prefix_len);
-    const int tiles = x.ntok > p.tile_tokens ? 2 : 1;
-    for (int s = 0; s < tiles && ok; ++s, ++q_it) {
-      const int slot = q_it & 1;
-      if (!warp_wait(sh, p, C::kQEmpty + slot, ((q_it >> 1) & 1) ^ 1, 3)) { ok = false; break; }
-      const uint32_t bar = smem_u32(sh.bars + C::kQFull + slot);
-      if (elect_one()) {
-        mbar_arrive_expect_tx(bar, q_bytes);
+  // One step per subtile, then two more for the last V tiles.
+  Item x{};
+  int it = 0, j = 0, s = 0, tiles = 1, left = 2;
+  bool more = true, ok = true;
+  while (ok) {
+    if (more && j == x.j1) {
+      more = take_item<D>(sh, p, it, x, 1);
+      if (!more && *reinterpret_cast<volatile int32_t*>(sh.abort_flag)) break;
+      if (more) {
+        ++it;
+        j = x.j0;
+        tiles = x.ntok > p.tile_tokens ? 2 : 1;
+        next = key_tile(p, x, j, prefix_len);
+        for (int i = 0; i < tiles && ok; ++i, ++q_it) {
+          const int slot = q_it & 1;
+          if (!warp_wait(sh, p, C::kQEmpty + slot, ((q_it >> 1) & 1) ^ 1, 3)) { ok = false; break; }
+          const uint32_t bar = smem_u32(sh.bars + C::kQFull + slot);
+          if (elect_one()) {
+            mbar_arrive_expect_tx(bar, q_bytes);
 #pragma unroll
-        for (int half = 0; half < C::kHalves; ++half)
-          tma_load_3d(smem_u32(q_tile<D>(sh, slot)) + half * kHalfBytes, tm_q, bar, 64 * half, x.head * p.group,
-                      x.tok0 + s * p.tile_tokens);
+            for (int half = 0; half < C::kHalves; ++half)
+              tma_load_3d(smem_u32(q_tile<D>(sh, slot)) + half * kHalfBytes, tm_q, bar, 64 * half, x.head * p.group,
+                          x.tok0 + i * p.tile_tokens);
+          }
+          __syncwarp();
+        }
       }
-      __syncwarp();
     }
-    for (int j = x.j0; j < x.j1 && ok; ++j) {
-      const KeyTile k = next;
+    if (more && s == 0) {
+      cur = next;
       if (j + 1 < x.j1) next = key_tile(p, x, j + 1, prefix_len);
-      for (int s = 0; s < tiles && ok; ++s) {
-        if (has2 && !fill(tm_v, v2, true)) ok = false;
-        if (ok && s == 0 && !fill(tm_k, k, false)) ok = false;
-        v2 = v1;
-        has2 = has1;
-        v1 = k;
-        has1 = s == 0;
-      }
     }
-  }
-  for (int e = 0; e < 2 && ok && !*reinterpret_cast<volatile int32_t*>(sh.abort_flag); ++e) {
-    if (has2 && !fill(tm_v, v2, true)) ok = false;
+#pragma unroll 1
+    for (int is_k = 0; is_k < 2 && ok; ++is_k) {
+      if (is_k ? !(more && s == 0) : !has2) continue;
+      const KeyTile k = is_k ? cur : v2;
+      const int st = kv_it % C::kStages;
+      if (!warp_wait(sh, p, C::kKVEmpty + st, ((kv_it / C::kStages) & 1) ^ 1, 2)) { ok = false; break; }
+      const bool raw = !is_k && (k.head_valid & 255) < 128;
+      load_tile<D>(sh, p, is_k ? tm_k : tm_v, k, st, raw ? C::kVRaw + st : C::kKVFull + st);
+      raw_last = raw ? raw_last | (1u << st) : raw_last & ~(1u << st);
+      if (raw) raw_phase ^= 1u << st;
+      ++kv_it;
+    }
     v2 = v1;
     has2 = has1;
-    has1 = false;
+    if (more) {
+      v1 = cur;
+      has1 = s == 0;
+      if (++s == tiles) {
+        s = 0;
+        ++j;
+      }
+    } else {
+      has1 = false;
+      if (--left == 0) break;
+    }
   }
   // The CTA must not exit with copies still landing in its shared memory: wait
   // for the last fill of every stage and Q slot, whoever gave up since.
@@ -515,39 +524,46 @@ __device__ __forceinline__ void zero_role(const Shared& sh, const Params& p) {
   int kv_it = 0;
   uint32_t raw_phase = 0;
   int32_t v1 = 0, v2 = 0;  // valid keys of the V tiles of the last two subtiles; 0: no new tile
-  auto pass_v = [&](int32_t valid) -> bool {
-    if (valid > 0 && valid < 128) {
+  Item x{};
+  int it = 0, j = 0, s = 0, tiles = 1, left = 2;
+  bool more = true;
+  for (;;) {
+    if (more && j == x.j1) {
+      more = take_item<D>(sh, p, it, x, 51);
+      if (!more && *reinterpret_cast<volatile int32_t*>(sh.abort_flag)) return;
+      if (more) {
+        ++it;
+        j = x.j0;
+        tiles = x.ntok > p.tile_tokens ? 2 : 1;
+      }
+    }
+    if (v2 > 0 && v2 < 128) {
       const int st = kv_it % C::kStages;
-      if (!warp_wait(sh, p, C::kVRaw + st, (raw_phase >> st) & 1, 50)) return false;
+      if (!warp_wait(sh, p, C::kVRaw + st, (raw_phase >> st) & 1, 50)) return;
       raw_phase ^= 1u << st;
-      const uint32_t base = smem_u32(kv_tile<D>(sh, st));
-      const int words = (128 - valid) * 8;  // 16-byte pieces per half
+      const uint32_t base = smem_u32(kv_tile<D>(sh, st)) + v2 * 128;
+      const int pieces = (128 - v2) * 8;  // of 16 bytes, in each half
 #pragma unroll
       for (int half = 0; half < C::kHalves; ++half)
-        for (int i = lane; i < words; i += 32) st_shared_v4(base + half * kHalfBytes + valid * 128 + i * 16, 0, 0, 0, 0);
+        for (int i = lane; i < pieces; i += 32) st_shared_v4(base + half * kHalfBytes + i * 16, 0, 0, 0, 0);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(sh.bars + C::kKVFull + st));
     }
-    kv_it += valid > 0;
-    return true;
-  };
-  Item x;
-  for (int it = 0; take_item<D>(sh, p, it, x, 51); ++it) {
-    const int tiles = x.ntok > p.tile_tokens ? 2 : 1;
-    for (int j = x.j0; j < x.j1; ++j) {
-      const int32_t valid = tile_keys(x, j, prefix_len);
-      for (int s = 0; s < tiles; ++s) {
-        if (!pass_v(v2)) return;
-        kv_it += s == 0;
-        v2 = v1;
-        v1 = s == 0 ? valid : 0;
+    kv_it += v2 > 0;
+    v2 = v1;
+    if (more) {
+      kv_it += s == 0;
+      v1 = s == 0 ? tile_keys(x, j, prefix_len) : 0;
+      if (++s == tiles) {
+        s = 0;
+        ++j;
       }
+    } else {
+      v1 = 0;
+      if (--left == 0) return;
     }
   }
-  if (*reinterpret_cast<volatile int32_t*>(sh.abort_flag)) return;
-  if (!pass_v(v2)) return;
-  pass_v(v1);
 }
 
 // ---------------------------------------------------------------- MMA issue
@@ -572,72 +588,75 @@ template <int D>
 __device__ __forceinline__ void mma_issuer(const Shared& sh, const Params& p, uint32_t tmem) {
   using C = Cfg<D>;
   int kv_it = 0, q_it = 0;
-  uint32_t p_phase = 0;  // bit t: parity of stream t's next P
-  uint32_t m = 0;        // subtile
-  uint32_t pv1 = 0, pv2 = 0;
-  int vst = 0;
-  bool ok = true;
+  uint32_t p_phase = 0;        // bit t: parity of stream t's next P
+  uint32_t pv1 = 0, pv2 = 0;   // flags of the last and the second last subtile
+  int vst = 0, kst = 0;
 
-  // PV of subtile m-2, on stream m & 1
-  auto issue_pv = [&](uint32_t pv) -> bool {
-    const uint32_t t = m & 1;
-    if (pv & kPvOpens) {
-      vst = kv_it % C::kStages;
-      if (!warp_wait(sh, p, C::kKVFull + vst, (kv_it / C::kStages) & 1, 12)) return false;
-      ++kv_it;
-    }
-    if (!warp_wait(sh, p, C::kPFull + t, (p_phase >> t) & 1, 14 + t)) return false;
-    p_phase ^= 1u << t;
-    tc_fence_after();
-    const uint64_t vd = smem_desc_sw128(smem_u32(kv_tile<D>(sh, vst)), kHalfBytes, 1024);
-    if (elect_one()) {
-      issue_pv_slice<D, 0>(tmem + 256 + 128 * t, tmem + 128 * t, vd, pv & kPvFirst ? 0u : 1u);
-      if (pv & kPvLast) mma_commit(smem_u32(sh.bars + C::kOFull + t));
-      if (pv & kPvCloses) mma_commit(smem_u32(sh.bars + C::kKVEmpty + vst));
-    }
-    __syncwarp();
-    return true;
-  };
-
-  Item x;
-  for (int it = 0; ok && take_item<D>(sh, p, it, x, 10); ++it) {
-    const int tiles = x.ntok > p.tile_tokens ? 2 : 1;
-    const int n = x.j1 - x.j0;
-    int kst = 0;
-    for (int j = 0; j < n && ok; ++j) {
-      for (int s = 0; s < tiles; ++s, ++m) {
-        const uint32_t t = m & 1;
-        if ((pv2 & kPvLive) && !issue_pv(pv2)) { ok = false; break; }
-        if (s == 0) {
-          kst = kv_it % C::kStages;
-          if (!warp_wait(sh, p, C::kKVFull + kst, (kv_it / C::kStages) & 1, 13)) { ok = false; break; }
-          ++kv_it;
-        }
-        const int slot = (q_it + s) & 1;
-        if (j == 0 && !warp_wait(sh, p, C::kQFull + slot, ((q_it + s) >> 1) & 1, 11)) { ok = false; break; }
-        tc_fence_after();
-        const uint64_t qd = smem_desc_sw128(smem_u32(q_tile<D>(sh, slot)), 16, 1024);
-        const uint64_t kd = smem_desc_sw128(smem_u32(kv_tile<D>(sh, kst)), 16, 1024);
-        if (elect_one()) {
-          issue_s_slice<D, 0>(tmem + 128 * t, qd, kd);
-          mma_commit(smem_u32(sh.bars + C::kSFull + t));
-          if (s == tiles - 1) mma_commit(smem_u32(sh.bars + C::kKVEmpty + kst));
-          if (j == n - 1) mma_commit(smem_u32(sh.bars + C::kQEmpty + slot));
-        }
-        __syncwarp();
-        pv2 = pv1;
-        // first and last subtile of its stream in this item
-        const int step = tiles == 2 ? 1 : 2;
-        pv1 = kPvLive | (j < step ? kPvFirst : 0u) | (j + step >= n ? kPvLast : 0u) | (s == 0 ? kPvOpens : 0u) |
-              (s == tiles - 1 ? kPvCloses : 0u);
+  // One step per subtile, then two more for the last PV products.
+  Item x{};
+  int it = 0, j = 0, n = 0, s = 0, tiles = 1, left = 2;
+  bool more = true;
+  for (uint32_t m = 0;; ++m) {
+    if (more && j == n) {
+      q_it += n > 0 ? tiles : 0;
+      more = take_item<D>(sh, p, it, x, 10);
+      if (!more && *reinterpret_cast<volatile int32_t*>(sh.abort_flag)) break;
+      if (more) {
+        ++it;
+        j = 0;
+        n = x.j1 - x.j0;
+        tiles = x.ntok > p.tile_tokens ? 2 : 1;
       }
     }
-    q_it += tiles;
-  }
-  for (int e = 0; e < 2 && ok && !*reinterpret_cast<volatile int32_t*>(sh.abort_flag); ++e, ++m) {
-    if ((pv2 & kPvLive) && !issue_pv(pv2)) ok = false;
+    const uint32_t t = m & 1;
+    if (pv2 & kPvLive) {
+      if (pv2 & kPvOpens) {
+        vst = kv_it % C::kStages;
+        if (!warp_wait(sh, p, C::kKVFull + vst, (kv_it / C::kStages) & 1, 12)) break;
+        ++kv_it;
+      }
+      if (!warp_wait(sh, p, C::kPFull + t, (p_phase >> t) & 1, 14 + t)) break;
+      p_phase ^= 1u << t;
+      tc_fence_after();
+      const uint64_t vd = smem_desc_sw128(smem_u32(kv_tile<D>(sh, vst)), kHalfBytes, 1024);
+      if (elect_one()) {
+        issue_pv_slice<D, 0>(tmem + 256 + 128 * t, tmem + 128 * t, vd, pv2 & kPvFirst ? 0u : 1u);
+        if (pv2 & kPvLast) mma_commit(smem_u32(sh.bars + C::kOFull + t));
+        if (pv2 & kPvCloses) mma_commit(smem_u32(sh.bars + C::kKVEmpty + vst));
+      }
+      __syncwarp();
+    }
     pv2 = pv1;
-    pv1 = 0;
+    if (!more) {
+      pv1 = 0;
+      if (--left == 0) break;
+      continue;
+    }
+    if (s == 0) {
+      kst = kv_it % C::kStages;
+      if (!warp_wait(sh, p, C::kKVFull + kst, (kv_it / C::kStages) & 1, 13)) break;
+      ++kv_it;
+    }
+    const int slot = (q_it + s) & 1;
+    if (j == 0 && !warp_wait(sh, p, C::kQFull + slot, ((q_it + s) >> 1) & 1, 11)) break;
+    tc_fence_after();
+    const uint64_t qd = smem_desc_sw128(smem_u32(q_tile<D>(sh, slot)), 16, 1024);
+    const uint64_t kd = smem_desc_sw128(smem_u32(kv_tile<D>(sh, kst)), 16, 1024);
+    if (elect_one()) {
+      issue_s_slice<D, 0>(tmem + 128 * t, qd, kd);
+      mma_commit(smem_u32(sh.bars + C::kSFull + t));
+      if (s == tiles - 1) mma_commit(smem_u32(sh.bars + C::kKVEmpty + kst));
+      if (j == n - 1) mma_commit(smem_u32(sh.bars + C::kQEmpty + slot));
+    }
+    __syncwarp();
+    // first and last subtile of its stream in this item
+    const int step = tiles == 2 ? 1 : 2;
+    pv1 = kPvLive | (j < step ? kPvFirst : 0u) | (j + step >= n ? kPvLast : 0u) | (s == 0 ? kPvOpens : 0u) |
+          (s == tiles - 1 ? kPvCloses : 0u);
+    if (++s == tiles) {
+      s = 0;
+      ++j;
+    }
   }
   // all issued MMAs complete before TMEM is released
   if (elect_one()) mma_commit(smem_u32(sh.bars + C::kMmaDone));
@@ -730,9 +749,15 @@ __device__ __forceinline__ void softmax_role(const Shared& sh, const Params& p, 
         }
         tmem_wait_ld();
         if (visible < 128) {
+          // bit c of word w: column 32 w + c is seen
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= visible) s[c] = -INFINITY;
+          for (int w = 0; w < 4; ++w) {
+            const int32_t n = visible - 32 * w;
+            const uint32_t bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!(bits >> c & 1)) s[32 * w + c] = -INFINITY;
+          }
         }
 #pragma unroll
         for (int c = 0; c < 8; ++c) mxs[c] = fmaxf(s[c], s[c + 8]);
@@ -749,7 +774,7 @@ __device__ __forceinline__ void softmax_role(const Shared& sh, const Params& p, 
           const bool need = m_new > m_ref + kRescaleThreshold;
           if (__any_sync(0xffffffffu, need)) {
             const float alpha = need ? fast_exp2(m_ref - m_new) : 1.0f;
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
               uint32_t r[32];
               tmem_ld32(o_tm + 32 * q, r);
@@ -794,7 +819,7 @@ __device__ __forceinline__ void softmax_role(const Shared& sh, const Params& p, 
     const float lse_row = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
     if (dest == kDirect) {
       uint4* dst = reinterpret_cast<uint4*>(p.out + (int64_t(tok) * p.H + head) * D);
-#pragma unroll
+#pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
         uint32_t r[32];
         tmem_ld32(o_tm + 32 * q, r);
@@ -828,7 +853,7 @@ __device__ __forceinline__ void softmax_role(const Shared& sh, const Params& p, 
     float* po = p.part_o + prow * D;
     if (!first) {
       float4* dst = reinterpret_cast<float4*>(po);
-#pragma unroll
+#pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
         uint32_t r[32];
         tmem_ld32(o_tm + 32 * q, r);
