@@ -42,6 +42,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
@@ -57,7 +58,8 @@ constexpr int kThreads = 384;
 constexpr uint32_t kSoftmaxRegs = 224;
 constexpr uint32_t kControlRegs = 56;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs == kThreads * 168, "register split must match launch");
-constexpr int kHalfBytes = 128 * 128;  // 128 rows x 64 bf16, 128-byte swizzled
+constexpr int kHalfBytes = 128 * 128;  // 64-column half of a Q tile: 128 rows x 64 bf16, 128-byte swizzled
+constexpr int kAtom = 8 * 128;         // 8 rows of 64 bf16: the swizzle's unit
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;
 constexpr float kLn2 = 0.69314718055994531f;
@@ -75,6 +77,14 @@ struct Item {
 };
 static_assert(sizeof(Item) == 48, "item layout");
 
+// A two-tile unit whose first cut is the beginning of the CTA's share.
+struct Cut {
+  int64_t s;        // cost position of the unit
+  int32_t head, tok0, ntok, ktiles;
+  int32_t c0, n;    // shares c0 .. c0+n-1 hold its tiles; n = 0: none
+};
+static_assert(sizeof(Cut) == WF_BATCH_CUT_BYTES, "cut record layout");
+
 struct Params {
   const wf_batch_hdr* hdr;
   const wf_batch_unit* units;
@@ -88,7 +98,7 @@ struct Params {
   wf_dev_status* status;
   float* part_o;    // partial rows: [prefix, own][key parity][ctok][H], then [CTA][head, tail][row tile or key parity][128]
   float* part_lse;
-  int2* cuts;       // per CTA: (key head, unit) that its first item continues, unit -1 for none
+  Cut* cuts;        // per CTA
   int64_t main_rows;
   uint64_t fingerprint;
   uint64_t timeout_ns;
@@ -101,6 +111,12 @@ template <int D>
 struct Cfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kTile = kHalves * kHalfBytes;
+  // K/V tiles hold 8-key groups one after another, in each the atoms of its
+  // 64-column halves: a page's rows are then one block, whatever its size, and
+  // one copy brings both halves.  (A copy takes about 60 cycles + 4 per
+  // 128-byte row: with 16-token pages and a copy per half, 3970 cycles for a K
+  // and a V tile, where HBM delivers them in 2950.)
+  static constexpr int kGroup = kHalves * kAtom;
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, 0);
   static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, 1);
@@ -176,11 +192,10 @@ __device__ __forceinline__ bool warp_wait(const Shared& sh, const Params& p, int
 }
 
 // ---------------------------------------------------------------- shares of the line of costs
-// Equal shares of `size` (the last one shorter); the division by it is a
-// multiplication by floor((2^64 - 1) / size), at most one below the quotient.
+// Equal shares of `size` (the last one shorter).
 struct Line {
   int64_t head_cost, total, size;
-  uint64_t inv;
+  double rcp;  // 1 / size
 };
 
 __device__ __forceinline__ Line line_of(const Params& p) {
@@ -189,7 +204,7 @@ __device__ __forceinline__ Line line_of(const Params& p) {
   x.head_cost = h->head_cost;
   x.total = h->head_cost * p.kv_heads;
   x.size = h->share;
-  x.inv = h->share_inv;
+  x.rcp = h->share_rcp;
   return x;
 }
 
@@ -198,9 +213,11 @@ __device__ __forceinline__ int64_t share_begin(const Line& x, int c) {
   return b < x.total ? b : x.total;
 }
 
-// The share that holds cost position s < total.
+// The share that holds cost position s < total: at most 256 of them, so the
+// fp64 product is off by far less than one.
 __device__ __forceinline__ int share_of(const Line& x, int64_t s) {
-  int c = int(__umul64hi(uint64_t(s), x.inv));
+  int c = int(double(s) * x.rcp);
+  c -= c * x.size > s;
   c += (c + 1) * x.size <= s;
   return c;
 }
@@ -275,14 +292,15 @@ __device__ __forceinline__ void scheduler(const Shared& sh, const Params& p) {
   const int lane = threadIdx.x & 31;
   int it = 0;
   int32_t parity = 0;
-  int32_t cut_unit = -1, cut_head = 0;
   const Line line = line_of(p);
   const int64_t head_cost = line.head_cost;
   const int units = p.hdr->units;
   const int c = int(blockIdx.x);
   const int64_t lo = share_begin(line, c), hi = share_begin(line, c + 1);
   if (p.hdr->fingerprint == p.fingerprint && lo < hi) {
-    int32_t head = int32_t(lo / head_cost);
+    int32_t head = int32_t(double(lo) / double(head_cost));  // at most 255: off by one at most
+    head -= head * head_cost > lo;
+    head += (head + 1) * head_cost <= lo;
     // first unit: the last one that starts at or before lo, found 32 probes at a time
     const int64_t rem = lo - int64_t(head) * head_cost;
     int32_t a = 0, b = units;
@@ -294,6 +312,27 @@ __device__ __forceinline__ void scheduler(const Shared& sh, const Params& p) {
       b = min(b, a + step);
     }
     int32_t u = a;
+    if (lane == 0) {
+      // for the merging, before anything is waited for
+      const wf_batch_unit r = p.units[u];
+      const int64_t s = int64_t(head) * head_cost + p.pre[u];
+      const int32_t w = tile_shift(r.ntok, p.tile_tokens);
+      Cut k{};
+      int32_t j0, j1;
+      share_tiles(s, w, r.ktiles, lo, hi, j0, j1);
+      if (j0 > 0 && j0 < j1 && r.req >= 0 && r.ntok > p.tile_tokens) {
+        k.c0 = share_of(line, s);
+        if (share_of(line, s + (int64_t(j0 - 1) << w)) == k.c0) {
+          k.s = s;
+          k.head = head;
+          k.tok0 = r.tok0;
+          k.ntok = r.ntok;
+          k.ktiles = r.ktiles;
+          k.n = share_of(line, s + (int64_t(r.ktiles - 1) << w)) - k.c0 + 1;
+        }
+      }
+      p.cuts[c] = k;
+    }
     bool more = true;
     while (more) {
       // 32 units at a time, one per lane
@@ -337,10 +376,6 @@ __device__ __forceinline__ void scheduler(const Shared& sh, const Params& p) {
                                                    : kMainOwn;
           sh.items[it % kItems] = x;
           mbar_arrive(smem_u32(sh.bars + Cfg<D>::kItemFull + it % kItems));
-          if (j0 > 0) {
-            cut_unit = mine;
-            cut_head = head;
-          }
         }
         __syncwarp();
         parity = (parity + n) & 1;
@@ -355,9 +390,6 @@ __device__ __forceinline__ void scheduler(const Shared& sh, const Params& p) {
       }
     }
   }
-  // only the first item can continue a unit
-  if (const uint32_t who = __ballot_sync(0xffffffffu, cut_unit >= 0); who ? lane == __ffs(who) - 1 : lane == 0)
-    p.cuts[c] = make_int2(cut_head, cut_unit);
   if (!warp_wait(sh, p, Cfg<D>::kItemEmpty + it % kItems, ((it / kItems) & 1) ^ 1, 41)) return;
   if (lane == 0) {
     Item x{};
@@ -367,12 +399,12 @@ __device__ __forceinline__ void scheduler(const Shared& sh, const Params& p) {
 }
 
 // ---------------------------------------------------------------- K/V tiles
-// Key tile j of an item.  Lane i of the producer holds the first pool token of
+// Key tile j of an item.  Lane i of the producer holds the pool position of
 // the tile's i-th page (16 at most): read from the table once, a tile ahead of
 // its use, for K and V both.
 struct KeyTile {
   int32_t head_valid;  // key head << 8 | keys (at most 128)
-  int32_t at;          // of this lane's page
+  int32_t at;          // this lane's page: its first 8-token group of the pool
 };
 
 __device__ __forceinline__ int32_t tile_keys(const Item& x, int32_t j, int32_t prefix_len) {
@@ -391,10 +423,21 @@ __device__ __forceinline__ KeyTile key_tile(const Params& p, const Item& x, int3
   k.at = 0;
   if (pg << p.page_shift < valid) {
     // an entry outside the pool reads zeros, not memory: the map's bounds hold
-    const int64_t tok = int64_t(__ldg(list + first + pg)) << p.page_shift;
-    k.at = tok < 0 || tok > 0x7FFFFF00 ? 0x7FFFFF00 : int32_t(tok);
+    const int64_t at = int64_t(__ldg(list + first + pg)) << (p.page_shift - 3);
+    k.at = at < 0 || at > 0x0FFFFFF0 ? 0x0FFFFFF0 : int32_t(at);
   }
   return k;
+}
+
+// One page's rows of one key head: coordinates (dim in half, key in group, half,
+// group, head).
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* tmap, uint32_t bar, int32_t head,
+                                              int32_t group) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %3, %3, %4, %5}], "
+      "[%2];" ::"r"(dst),
+      "l"(tmap), "r"(bar), "r"(0), "r"(group), "r"(head)
+      : "memory");
 }
 
 // Copies a tile; only pages that hold keys are read.  The pages go round by
@@ -405,16 +448,13 @@ __device__ __forceinline__ void load_tile(const Shared& sh, const Params& p, con
                                           int st, int bar_index) {
   const int head = k.head_valid >> 8, valid = k.head_valid & 255;
   const int pages = (valid + (1 << p.page_shift) - 1) >> p.page_shift;
-  const uint32_t page_bytes = 128u << p.page_shift;  // of one half
+  const uint32_t page_bytes = uint32_t(Cfg<D>::kHalves * 128) << p.page_shift;
   const uint32_t bar = smem_u32(sh.bars + bar_index);
   uint32_t dst = smem_u32(kv_tile<D>(sh, st));
-  if (elect_one()) mbar_arrive_expect_tx(bar, uint32_t(pages) * page_bytes * Cfg<D>::kHalves);
+  if (elect_one()) mbar_arrive_expect_tx(bar, uint32_t(pages) * page_bytes);
   for (int pg = 0; pg < pages; ++pg, dst += page_bytes) {
     const int32_t at = __shfl_sync(0xffffffffu, k.at, pg);
-    if (elect_one()) {
-      tma_load_3d(dst, tm, bar, 0, head, at);
-      if (Cfg<D>::kHalves == 2) tma_load_3d(dst + kHalfBytes, tm, bar, 64, head, at);
-    }
+    if (elect_one()) tma_load_page(dst, tm, bar, head, at);
   }
 }
 
@@ -513,9 +553,8 @@ __device__ __forceinline__ void producer(const Shared& sh, const Params& p, cons
   }
 }
 
-// Zero the rows behind the last key of ragged V tiles.  Row r of a 64-column
-// half is the 128 bytes at r * 128 (the swizzle permutes 16-byte pieces inside
-// a row only).
+// Zero the rows behind the last key of ragged V tiles (the swizzle permutes
+// 16-byte pieces inside a row's 128 bytes only).
 template <int D>
 __device__ __forceinline__ void zero_role(const Shared& sh, const Params& p) {
   using C = Cfg<D>;
@@ -541,11 +580,12 @@ __device__ __forceinline__ void zero_role(const Shared& sh, const Params& p) {
       const int st = kv_it % C::kStages;
       if (!warp_wait(sh, p, C::kVRaw + st, (raw_phase >> st) & 1, 50)) return;
       raw_phase ^= 1u << st;
-      const uint32_t base = smem_u32(kv_tile<D>(sh, st)) + v2 * 128;
-      const int pieces = (128 - v2) * 8;  // of 16 bytes, in each half
+      const uint32_t base = smem_u32(kv_tile<D>(sh, st)) + (lane & 7) * 16;
+      for (int row = v2 + (lane >> 3); row < 128; row += 4) {
 #pragma unroll
-      for (int half = 0; half < C::kHalves; ++half)
-        for (int i = lane; i < pieces; i += 32) st_shared_v4(base + half * kHalfBytes + i * 16, 0, 0, 0, 0);
+        for (int half = 0; half < C::kHalves; ++half)
+          st_shared_v4(base + (row >> 3) * C::kGroup + half * kAtom + (row & 7) * 128, 0, 0, 0, 0);
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(sh.bars + C::kKVFull + st));
@@ -570,14 +610,15 @@ __device__ __forceinline__ void zero_role(const Shared& sh, const Params& p) {
 // Descriptor offsets as immediates, fully unrolled (attn_sm100.cu measures why).
 template <int D, int kk>
 __device__ __forceinline__ void issue_s_slice(uint32_t s_tmem, uint64_t qd, uint64_t kd) {
-  constexpr uint32_t off = uint32_t(((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4);
-  mma_ss_off<off, off>(s_tmem, qd, kd, Cfg<D>::kIdescQK, kk > 0 ? 1u : 0u);
+  constexpr uint32_t q_off = uint32_t(((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4);
+  constexpr uint32_t k_off = uint32_t(((kk >> 2) * kAtom + (kk & 3) * 32) >> 4);
+  mma_ss_off<q_off, k_off>(s_tmem, qd, kd, Cfg<D>::kIdescQK, kk > 0 ? 1u : 0u);
   if constexpr (kk + 1 < D / 16) issue_s_slice<D, kk + 1>(s_tmem, qd, kd);
 }
 
 template <int D, int kk>
 __device__ __forceinline__ void issue_pv_slice(uint32_t o_tmem, uint32_t p_tmem, uint64_t vd, uint32_t acc0) {
-  mma_ts_off<kk * 8, uint32_t((kk * 2048) >> 4)>(o_tmem, p_tmem, vd, Cfg<D>::kIdescPV, kk > 0 ? 1u : acc0);
+  mma_ts_off<kk * 8, uint32_t((kk * 2 * Cfg<D>::kGroup) >> 4)>(o_tmem, p_tmem, vd, Cfg<D>::kIdescPV, kk > 0 ? 1u : acc0);
   if constexpr (kk < 7) issue_pv_slice<D, kk + 1>(o_tmem, p_tmem, vd, acc0);
 }
 
@@ -618,7 +659,7 @@ __device__ __forceinline__ void mma_issuer(const Shared& sh, const Params& p, ui
       if (!warp_wait(sh, p, C::kPFull + t, (p_phase >> t) & 1, 14 + t)) break;
       p_phase ^= 1u << t;
       tc_fence_after();
-      const uint64_t vd = smem_desc_sw128(smem_u32(kv_tile<D>(sh, vst)), kHalfBytes, 1024);
+      const uint64_t vd = smem_desc_sw128(smem_u32(kv_tile<D>(sh, vst)), kAtom, C::kGroup);
       if (elect_one()) {
         issue_pv_slice<D, 0>(tmem + 256 + 128 * t, tmem + 128 * t, vd, pv2 & kPvFirst ? 0u : 1u);
         if (pv2 & kPvLast) mma_commit(smem_u32(sh.bars + C::kOFull + t));
@@ -640,8 +681,8 @@ __device__ __forceinline__ void mma_issuer(const Shared& sh, const Params& p, ui
     const int slot = (q_it + s) & 1;
     if (j == 0 && !warp_wait(sh, p, C::kQFull + slot, ((q_it + s) >> 1) & 1, 11)) break;
     tc_fence_after();
-    const uint64_t qd = smem_desc_sw128(smem_u32(q_tile<D>(sh, slot)), 16, 1024);
-    const uint64_t kd = smem_desc_sw128(smem_u32(kv_tile<D>(sh, kst)), 16, 1024);
+    const uint64_t qd = smem_desc_sw128(smem_u32(q_tile<D>(sh, slot)), 16, kAtom);
+    const uint64_t kd = smem_desc_sw128(smem_u32(kv_tile<D>(sh, kst)), 16, C::kGroup);
     if (elect_one()) {
       issue_s_slice<D, 0>(tmem + 128 * t, qd, kd);
       mma_commit(smem_u32(sh.bars + C::kSFull + t));
@@ -894,6 +935,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
+  // the merging kernel may come onto this SM as soon as this block leaves it
+  cudaTriggerProgrammaticLaunchCompletion();
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.hdr->fingerprint != p.fingerprint)
     p.status->code = WF_ERR_PLAN;  // not built, or for another description: the scheduler finds no work
   if (warp == 8) {
@@ -928,11 +971,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- merging parts
-// One warp per row.  A row's parts, in this order: its own unit's shares, then
-// (rows of small requests) the shares of the prefix unit that holds its token.
-// Up to 32 parts at a time: lane i finds part i's row and LSE, the warp their
-// maximum and weights, and the O rows are then summed four dims per lane, the
-// loads independent of one another.
+// A warp merges up to kRows neighbouring rows that have the same parts (the
+// query heads of one token and key head, rows of a two-tile unit).  The parts,
+// in this order: the rows' own unit's shares, then (small requests) the shares
+// of the prefix unit that holds their token.  Up to 32 parts at a time: lane i
+// finds part i's first row and LSEs, the warp their maxima and weights, and the
+// O rows are then summed, D / 32 dims per lane, kRows * kAhead loads in flight.
 struct Parts {
   int64_t s;      // cost position of the unit
   int32_t shift, ktiles;
@@ -968,96 +1012,129 @@ __device__ __forceinline__ int64_t part_row(const Params& p, const Line& line, c
   return j0 < j1 ? cut_row(p, c, j0 == 0, half, q.row) : -1;
 }
 
-template <int D>
-__device__ __forceinline__ void merge_row(const Params& p, const Line& line, const Parts& a, const Parts& b, int32_t ct,
-                                          int32_t tok, int32_t head) {
-  constexpr int V = D / 32;  // dims per lane
+template <int V>
+__device__ __forceinline__ void load_part(float (&o)[V], const float* row, int lane) {
+  if constexpr (V == 4) {
+    const float4 f = __ldcs(reinterpret_cast<const float4*>(row) + lane);
+    o[0] = f.x; o[1] = f.y; o[2] = f.z; o[3] = f.w;
+  } else {
+    const float2 f = __ldcs(reinterpret_cast<const float2*>(row) + lane);
+    o[0] = f.x; o[1] = f.y;
+  }
+}
+
+// ct, head0: of the first row, where parts lie by token and head; nr: rows;
+// tok, head: where each row's result goes.
+template <int D, int kRows>
+__device__ __forceinline__ void merge_rows(const Params& p, const Line& line, const Parts& a, const Parts& b, int32_t ct,
+                                           int32_t head0, int nr, const int32_t (&tok)[kRows],
+                                           const int32_t (&head)[kRows]) {
+  constexpr int V = D / 32;
+  constexpr int kAhead = kRows == 1 ? 4 : 1;
   const int lane = threadIdx.x & 31;
-  float m = -INFINITY, l = 0.f;
-  float acc[V];
+  float m[kRows], l[kRows], acc[kRows][V];
 #pragma unroll
-  for (int k = 0; k < V; ++k) acc[k] = 0.f;
+  for (int r = 0; r < kRows; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[r][k] = 0.f;
+  }
   const int n = a.n + b.n;
   for (int base = 0; base < n; base += 32) {
     const int i = base + lane;
     int64_t row = -1;
     if (i < a.n)
-      row = part_row(p, line, a, i, ct, head);
+      row = part_row(p, line, a, i, ct, head0);
     else if (i < n)
-      row = part_row(p, line, b, i - a.n, ct, head);
-    const float x = row >= 0 ? p.part_lse[row] : -INFINITY;
-    float mx = x;
+      row = part_row(p, line, b, i - a.n, ct, head0);
+    float w[kRows];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    if (mx == -INFINITY) continue;
-    const float m_new = fmaxf(m, mx);
-    const float old = m == -INFINITY ? 0.f : expf(m - m_new);
-    const float w = x == -INFINITY ? 0.f : expf(x - m_new);
-    float ws = w;
+    for (int r = 0; r < kRows; ++r) w[r] = row >= 0 && r < nr ? p.part_lse[row + r] : -INFINITY;
+    uint32_t todo = 0;  // a part that saw no key of a row has no O row: its weight is 0 and it is not read
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, off);
-    l = l * old + ws;
-    m = m_new;
+    for (int r = 0; r < kRows; ++r) {
+      float mx = w[r];
 #pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] *= old;
-    // a part that saw no key has no O row
-    uint32_t todo = __ballot_sync(0xffffffffu, x != -INFINITY);
+      for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      todo |= __ballot_sync(0xffffffffu, w[r] != -INFINITY);
+      const float m_new = fmaxf(m[r], mx);
+      const float old = m[r] == -INFINITY ? 0.f : expf(m[r] - m_new);
+      w[r] = w[r] == -INFINITY ? 0.f : expf(w[r] - m_new);
+      float ws = w[r];
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, off);
+      l[r] = l[r] * old + ws;
+      m[r] = m_new;
+#pragma unroll
+      for (int k = 0; k < V; ++k) acc[r][k] *= old;
+    }
     while (todo) {
-      float o[4][V], wk[4];
+      float o[kAhead][kRows][V], wk[kAhead][kRows];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int src = todo ? __ffs(todo) - 1 : 0;
+      for (int k = 0; k < kAhead; ++k) {
         const bool any = todo != 0;
+        const int src = any ? __ffs(todo) - 1 : 0;
         todo &= todo - 1;
-        wk[k] = any ? __shfl_sync(0xffffffffu, w, src) : 0.f;
-        const int64_t r = __shfl_sync(0xffffffffu, row, src);
-        if (any) {
-          if constexpr (V == 4) {
-            const float4 f = reinterpret_cast<const float4*>(p.part_o + r * D)[lane];
-            o[k][0] = f.x; o[k][1] = f.y; o[k][2] = f.z; o[k][3] = f.w;
-          } else {
-            const float2 f = reinterpret_cast<const float2*>(p.part_o + r * D)[lane];
-            o[k][0] = f.x; o[k][1] = f.y;
-          }
-        } else {
+        const int64_t first = __shfl_sync(0xffffffffu, row, src);
 #pragma unroll
-          for (int v = 0; v < V; ++v) o[k][v] = 0.f;
+        for (int r = 0; r < kRows; ++r) {
+          const float x = __shfl_sync(0xffffffffu, w[r], src);
+          wk[k][r] = any ? x : 0.f;
+          if (wk[k][r] != 0.f) {
+            load_part<V>(o[k][r], p.part_o + (first + r) * D, lane);
+          } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[k][r][v] = 0.f;
+          }
         }
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < kAhead; ++k)
 #pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = fmaf(wk[k], o[k][v], acc[v]);
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[r][v] = fmaf(wk[k][r], o[k][r][v], acc[r][v]);
     }
   }
-  const float inv = l > 0.f ? 1.0f / l : 0.f;
-  __nv_bfloat16* dst = p.out + (int64_t(tok) * p.H + head) * D;
-  if constexpr (V == 4) {
-    uint2 o;
-    o.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    o.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-    reinterpret_cast<uint2*>(dst)[lane] = o;
-  } else {
-    reinterpret_cast<uint32_t*>(dst)[lane] = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    if (r >= nr) break;
+    const float inv = l[r] > 0.f ? 1.0f / l[r] : 0.f;
+    __nv_bfloat16* dst = p.out + (int64_t(tok[r]) * p.H + head[r]) * D;
+    if constexpr (V == 4) {
+      uint2 o;
+      o.x = pack_bf16x2(acc[r][0] * inv, acc[r][1] * inv);
+      o.y = pack_bf16x2(acc[r][2] * inv, acc[r][3] * inv);
+      reinterpret_cast<uint2*>(dst)[lane] = o;
+    } else {
+      reinterpret_cast<uint32_t*>(dst)[lane] = pack_bf16x2(acc[r][0] * inv, acc[r][1] * inv);
+    }
+    if (lane == 0 && p.lse)
+      p.lse[int64_t(head[r]) * p.max_tokens + tok[r]] = l[r] > 0.f ? m[r] + logf(l[r]) : -INFINITY;
   }
-  if (lane == 0 && p.lse) p.lse[int64_t(head) * p.max_tokens + tok] = l > 0.f ? m + logf(l) : -INFINITY;
 }
 
 constexpr int kCombineThreads = 256;
 constexpr int kCombineWarps = kCombineThreads / 32;
 
+// Launched while the attention still runs (programmatic dependent launch): what
+// does not depend on its results is read first.
 template <int D>
-__global__ void __launch_bounds__(kCombineThreads) batch_combine_kernel(const Params p) {
+__global__ void __launch_bounds__(kCombineThreads, 3) batch_combine_kernel(const Params p) {
   const wf_batch_hdr* h = p.hdr;
   const Line line = line_of(p);
-  if (h->fingerprint != p.fingerprint || line.total == 0) return;
+  const bool nothing = h->fingerprint != p.fingerprint || line.total == 0;
   const int warp = threadIdx.x >> 5;
   const int np = h->prefix_units;
+  const int64_t rows = int64_t(h->ctoks) * p.H;  // at most 2^20 tokens x 2^12 heads
+  const int64_t first = int64_t(blockIdx.x) * kCombineWarps + warp, stride = int64_t(gridDim.x) * kCombineWarps;
+  const int ctas = h->ctas;
   Parts none{};
+  bool waited = false;
   // rows of one-tile units, a warp each
-  const int64_t rows = int64_t(h->ctoks) * p.H;
-  for (int64_t k = int64_t(blockIdx.x) * kCombineWarps + warp; k < rows; k += int64_t(gridDim.x) * kCombineWarps) {
-    const int32_t ct = int32_t(uint32_t(k) / uint32_t(p.H)), head = int32_t(uint32_t(k) - uint32_t(ct) * uint32_t(p.H));
+  for (int64_t k = first; k < rows && !nothing; k += stride) {
+    const int32_t ct = int32_t(uint64_t(k) / uint32_t(p.H)), head = int32_t(k - int64_t(ct) * p.H);
     const wf_batch_ctok at = p.ctok_list[ct];
     const int32_t pu = at.tok / (2 * p.tile_tokens);
     const wf_batch_unit u = p.units[at.unit], q = p.units[pu < np ? pu : at.unit];
@@ -1067,23 +1144,36 @@ __global__ void __launch_bounds__(kCombineThreads) batch_combine_kernel(const Pa
     const int64_t s0 = int64_t(kv) * line.head_cost;
     const Parts a = parts_of(p, line, u, s0 + pre_u, at.tok - u.tok0, row_head);
     const Parts b = u.ptiles < 0 ? parts_of(p, line, q, s0 + pre_q, at.tok - q.tok0, row_head) : none;
-    merge_row<D>(p, line, a, b, ct, at.tok, head);
+    if (!waited) cudaGridDependencySynchronize();
+    waited = true;
+    const int32_t toks[1] = {at.tok}, heads[1] = {head};
+    merge_rows<D, 1>(p, line, a, b, ct, head, 1, toks, heads);
   }
-  // rows of two-tile units that were cut, a block for 8 rows; a unit is taken up at its first cut
-  if (p.max_tokens <= p.tile_tokens) return;
-  constexpr int kGroups = 256 / kCombineWarps;
-  for (int k = blockIdx.x; k < h->ctas * kGroups; k += gridDim.x) {
-    const int c = k / kGroups, r = k % kGroups * kCombineWarps + warp;
-    const int2 cut = p.cuts[c];
-    // (out of range only where a CTA gave up before it noted its cut)
-    if (cut.y < 0 || cut.y >= h->units || cut.x < 0 || cut.x >= p.kv_heads) continue;
-    const wf_batch_unit u = p.units[cut.y];
-    if (u.req < 0 || u.ntok <= p.tile_tokens || r >= u.ntok * p.group) continue;
-    const int32_t tok_i = r / p.group, row_head = r - tok_i * p.group;
-    const Parts a = parts_of(p, line, u, int64_t(cut.x) * line.head_cost + p.pre[cut.y], tok_i, row_head);
-    bool first = true;
-    for (int d = a.c0 + 1; d < c; ++d) first &= p.cuts[d].y < 0;
-    if (first) merge_row<D>(p, line, a, none, 0, u.tok0 + tok_i, cut.x * p.group + row_head);
+  if (!waited) cudaGridDependencySynchronize();
+  // rows of two-tile units that were cut, a warp for four rows of a tile; a unit is taken up at its first cut
+  if (p.max_tokens <= p.tile_tokens || nothing) return;
+  for (int k = int(first); k < ctas * 64; k += int(stride)) {
+    const int half = (k >> 5) & 1, row0 = (k & 31) * 4;
+    const Cut cut = p.cuts[k >> 6];
+    const int32_t live = (half ? cut.ntok - p.tile_tokens : p.tile_tokens) * p.group;
+    if (cut.n == 0 || row0 >= live) continue;
+    Parts a;
+    a.s = cut.s;
+    a.shift = WF_BATCH_PAIR_SHIFT;
+    a.ktiles = cut.ktiles;
+    a.c0 = cut.c0;
+    a.n = cut.n;
+    a.pair = a.cut = a.own = true;
+    a.half = half;
+    a.row = row0;
+    int32_t tok[4], head[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int32_t ti = (row0 + r) / p.group;
+      tok[r] = cut.tok0 + (half ? p.tile_tokens : 0) + ti;
+      head[r] = cut.head * p.group + (row0 + r - ti * p.group);
+    }
+    merge_rows<D, 4>(p, line, a, none, 0, 0, min(4, live - row0), tok, head);
   }
 }
 
@@ -1103,18 +1193,33 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
   return fn;
 }
 
-// [tokens, heads, D] with boxes of 64 dims x box_heads x box_tokens.
-bool make_tmap(CUtensorMap* tm, const void* base, int64_t tokens, int32_t heads, int32_t dim, int32_t box_heads,
-               int32_t box_tokens) {
+bool encode_map(CUtensorMap* tm, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                const cuuint32_t* box) {
   auto encode = get_encode();
-  if (!encode) return false;
-  cuuint64_t dims[3] = {cuuint64_t(dim), cuuint64_t(heads), cuuint64_t(tokens)};
-  cuuint64_t strides[2] = {cuuint64_t(dim) * 2, cuuint64_t(heads) * cuuint64_t(dim) * 2};
-  cuuint32_t box[3] = {64, cuuint32_t(box_heads), cuuint32_t(box_tokens)};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  return encode && encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void*>(base), dims, strides,
+                          box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// q [tokens, heads, D]: boxes of 64 dims x group heads x tile_tokens tokens.
+bool make_q_map(CUtensorMap* tm, const void* base, int64_t tokens, int32_t heads, int32_t dim, int32_t group,
+                int32_t tile_tokens) {
+  const cuuint64_t row = cuuint64_t(dim) * 2;
+  const cuuint64_t dims[3] = {cuuint64_t(dim), cuuint64_t(heads), cuuint64_t(tokens)};
+  const cuuint64_t strides[2] = {row, row * heads};
+  const cuuint32_t box[3] = {64, cuuint32_t(group), cuuint32_t(tile_tokens)};
+  return encode_map(tm, base, 3, dims, strides, box);
+}
+
+// A pool [tokens, heads, D] as (64 dims, 8 tokens, halves, groups of 8 tokens,
+// heads); a box is one head's rows of a page.
+bool make_pool_map(CUtensorMap* tm, const void* base, int64_t tokens, int32_t heads, int32_t dim, int32_t page) {
+  const cuuint64_t row = cuuint64_t(dim) * 2, token = row * heads;
+  const cuuint64_t dims[5] = {64, 8, cuuint64_t(dim / 64), cuuint64_t(tokens / 8), cuuint64_t(heads)};
+  const cuuint64_t strides[4] = {token, 128, 8 * token, row};
+  const cuuint32_t box[5] = {64, 8, cuuint32_t(dim / 64), cuuint32_t(page / 8), 1};
+  return encode_map(tm, base, 5, dims, strides, box);
 }
 
 template <int D>
@@ -1134,17 +1239,28 @@ wf_status launch(const wf_batch_desc* d, const BatchLayout& L, const Params& p, 
   }
   const int64_t pool = int64_t(d->pool_pages) * d->page_tokens;
   CUtensorMap tq, tk, tv;
-  if (!make_tmap(&tq, q, d->max_tokens, d->num_heads, D, L.group, L.tile_tokens) ||
-      !make_tmap(&tk, k_pool, pool, d->num_kv_heads, D, 1, d->page_tokens) ||
-      !make_tmap(&tv, v_pool, pool, d->num_kv_heads, D, 1, d->page_tokens))
+  if (!make_q_map(&tq, q, d->max_tokens, d->num_heads, D, L.group, L.tile_tokens) ||
+      !make_pool_map(&tk, k_pool, pool, d->num_kv_heads, D, d->page_tokens) ||
+      !make_pool_map(&tv, v_pool, pool, d->num_kv_heads, D, d->page_tokens))
     return WF_ERR_CUDA;
   batch_attn_kernel<D><<<L.ctas, kThreads, Cfg<D>::kSmemBytes, stream>>>(tq, tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return WF_ERR_CUDA;
-  // a warp per row that can need merging, as long as they run at once
-  const int64_t rows = int64_t(L.max_ctok) * d->num_heads + (d->max_tokens > L.tile_tokens ? int64_t(L.ctas) * 256 : 0);
-  const int64_t blocks = (rows + kCombineThreads / 32 - 1) / (kCombineThreads / 32);
-  const int64_t most = int64_t(L.ctas) * 8;
-  batch_combine_kernel<D><<<unsigned(blocks < most ? blocks : most), kCombineThreads, 0, stream>>>(p);
+  // a warp per merge_rows that can be needed, as long as they run at once
+  const int64_t warps = std::max(L.max_ctok * d->num_heads, d->max_tokens > L.tile_tokens ? int64_t(L.ctas) * 64 : 0);
+  const int64_t blocks = (warps + kCombineWarps - 1) / kCombineWarps, most = int64_t(L.ctas) * 8;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(blocks < most ? blocks : most));
+  cfg.blockDim = dim3(kCombineThreads);
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, batch_combine_kernel<D>, p) != cudaSuccess) {
+    cudaGetLastError();
+    return WF_ERR_CUDA;
+  }
   return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
 }
 
@@ -1192,7 +1308,7 @@ extern "C" wf_status wf_batch_attn(const wf_batch_desc* desc, const void* plan, 
   p.status = reinterpret_cast<wf_dev_status*>(ws);
   p.part_o = reinterpret_cast<float*>(ws + WF_ATTN_STATUS_BYTES);
   p.part_lse = reinterpret_cast<float*>(ws + L.off_lse);
-  p.cuts = reinterpret_cast<int2*>(ws + L.off_cuts);
+  p.cuts = reinterpret_cast<wf::Cut*>(ws + L.off_cuts);
   p.main_rows = L.main_rows;
   p.fingerprint = L.fingerprint;
   p.timeout_ns = wf::wait_timeout_ns();

@@ -27,9 +27,6 @@
 
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
-
 struct TablesParams {
   const int32_t* cached;
   const int32_t* fresh;
@@ -54,8 +51,10 @@ struct TablesParams {
 };
 
 // Exclusive block-wide sums of N 64-bit values per thread; totals in `total`.
-template <int N>
+// scratch: N * (warps + 1) values.
+template <int N, int kThreads>
 __device__ void block_scan(int64_t (&v)[N], int64_t (&total)[N], int64_t* scratch) {
+  constexpr int kWarps = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t inc[N];
 #pragma unroll
@@ -66,23 +65,50 @@ __device__ void block_scan(int64_t (&v)[N], int64_t (&total)[N], int64_t* scratc
       const int64_t o = __shfl_up_sync(0xffffffffu, inc[k], off);
       if (lane >= off) inc[k] += o;
     }
-    if (lane == 31) scratch[k * kWarps + warp] = inc[k];
+    if (lane == 31) scratch[k * (kWarps + 1) + warp] = inc[k];
+  }
+  __syncthreads();
+  // one warp per value turns the warps' sums into exclusive ones
+  if (warp < N) {
+    int64_t* row = scratch + warp * (kWarps + 1);
+    const int64_t own = lane < kWarps ? row[lane] : 0;
+    int64_t w = own;
+#pragma unroll
+    for (int off = 1; off < kWarps; off <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, w, off);
+      if (lane >= off) w += o;
+    }
+    if (lane < kWarps) row[lane] = w - own;
+    if (lane == kWarps - 1) row[kWarps] = w;
   }
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    int64_t w = scratch[k * kWarps + lane];  // every warp sums the warps' totals itself
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, w, off);
-      if (lane >= off) w += o;
-    }
-    total[k] = __shfl_sync(0xffffffffu, w, 31);
-    const int64_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
-    v[k] = inc[k] - v[k] + (warp > 0 ? before : 0);
+    v[k] = inc[k] - v[k] + scratch[k * (kWarps + 1) + warp];
+    total[k] = scratch[k * (kWarps + 1) + kWarps];
   }
   __syncthreads();  // scratch may be used again
 }
+
+// What a request adds to the sums, packed in three words so that the scan
+// (64-bit shuffles, the block's main instruction load at 1024 requests) stays
+// short: new tokens; new pages << 24 | tokens of one-tile units; own units <<
+// 16 | small requests.  With f <= 2^22, at most 2^24 pages a request and 2^13
+// requests no field reaches its neighbour (2^20 one-tile tokens, 2^13 small).
+struct Sums {
+  int64_t w[3];
+  __device__ __forceinline__ void add(int32_t f, int32_t new_pages, int32_t tile_tokens, int32_t group) {
+    const int32_t tiles = (f + tile_tokens - 1) / tile_tokens;
+    w[0] += f;
+    w[1] += (int64_t(new_pages) << 24) + ((tiles & 1) ? f - (tiles - 1) * tile_tokens : 0);
+    w[2] += (int64_t((tiles + 1) / 2) << 16) + (f > 0 && 2 * int64_t(f) * group <= 128);
+  }
+};
+__device__ __forceinline__ int64_t sum_tokens(const int64_t (&w)[3]) { return w[0]; }
+__device__ __forceinline__ int64_t sum_pages(const int64_t (&w)[3]) { return w[1] >> 24; }
+__device__ __forceinline__ int32_t sum_ctok(const int64_t (&w)[3]) { return int32_t(w[1] & 0xffffff); }
+__device__ __forceinline__ int64_t sum_units(const int64_t (&w)[3]) { return w[2] >> 16; }
+__device__ __forceinline__ int32_t sum_small(const int64_t (&w)[3]) { return int32_t(w[2] & 0xffff); }
 
 // Last index i in [0, n) with a[i] <= x (a ascending, a[0] <= x).
 __device__ __forceinline__ int last_not_above(const int32_t* a, int n, int32_t x) {
@@ -99,48 +125,45 @@ __device__ __forceinline__ int last_not_above(const int32_t* a, int n, int32_t x
 
 __device__ __forceinline__ int32_t ceil_shift(int64_t x, int s) { return int32_t((x + (int64_t(1) << s) - 1) >> s); }
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesParams p) {
   extern __shared__ int32_t sm[];
   int32_t* s_start = sm;                // [B + 1] first token of each request
   int32_t* s_first = s_start + p.B + 1; // [B] first new page of each request, from free_head
   int32_t* s_ctok = s_first + p.B;      // [B] first partial-row token
-  int32_t* s_unit = s_ctok + p.B;       // [B + 1] first own unit (block 0)
-  __shared__ int64_t scratch[5 * kWarps];
+  int32_t* s_unit = s_ctok + p.B;       // [B + 1] first own unit
+  __shared__ int64_t scratch[3 * (kThreads / 32 + 1)];
 
   const int tid = threadIdx.x;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
   const int Tt = p.tile_tokens;
-  const int32_t prefix = p.prefix_len ? *p.prefix_len : 0;
-  const int32_t head = *p.free_head;
+  const int32_t prefix = p.prefix_len ? __ldg(p.prefix_len) : 0;
+  const int32_t head = __ldg(p.free_head);
 
-  // sums over requests: new tokens, new pages, tokens of one-tile units, own units, small requests
-  int64_t v[5] = {0, 0, 0, 0, 0}, total[5];
-  int bad = 0;
+  Sums v{};
+  int64_t total[3];
+  int bad = 0;  // 1: invalid, 2: does not fit
   for (int b = b0; b < b1; ++b) {
-    const int64_t c = p.cached[b], f = p.fresh[b];
-    const int64_t h = p.held ? p.held[b] : (c < 0 ? 0 : ceil_shift(c, p.page_shift));
-    if (c < 0 || f < 0 || h < (c < 0 ? 0 : ceil_shift(c, p.page_shift))) {
+    const int32_t c = __ldg(p.cached + b), f = __ldg(p.fresh + b);
+    const int32_t least = c < 0 ? 0 : ceil_shift(c, p.page_shift);
+    const int32_t h = p.held ? __ldg(p.held + b) : least;
+    if (c < 0 || f < 0 || h < least) {
       bad |= 1;
       continue;
     }
-    const int64_t n = max(h, int64_t(ceil_shift(c + f, p.page_shift)));
-    if (n > p.cols) {
+    const int32_t n = max(h, ceil_shift(int64_t(c) + f, p.page_shift));
+    if (n > p.cols || f > p.max_tokens) {
       bad |= 2;
       continue;
     }
-    const int64_t tiles = (f + Tt - 1) / Tt;
-    v[0] += f;
-    v[1] += n - h;
-    v[2] += (tiles & 1) ? f - (tiles - 1) * Tt : 0;
-    v[3] += (tiles + 1) / 2;
-    v[4] += f > 0 && 2 * f * p.group <= 128;
+    v.add(f, n - h, Tt, p.group);
   }
-  block_scan<5>(v, total, scratch);
+  block_scan<3, kThreads>(v.w, total, scratch);
   if (prefix < 0 || head < 0) bad |= 1;
-  if (prefix > p.max_prefix || total[0] > p.max_tokens || head + total[1] > p.num_free) bad |= 2;
-  bad = (__syncthreads_or(bad & 1) ? 1 : 0) | (__syncthreads_or(bad & 2) ? 2 : 0);
-  if (bad) {
+  if (prefix > p.max_prefix || sum_tokens(total) > p.max_tokens || head + sum_pages(total) > p.num_free) bad |= 2;
+  if (__syncthreads_or(bad)) {
+    bad = __syncthreads_or(bad & 1);
     if (blockIdx.x == 0) {
       for (int b = tid; b <= p.B; b += kThreads) p.token_start[b] = 0;
       if (p.held_out)
@@ -148,9 +171,8 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesPara
       if (tid == 0) {
         *p.free_head_out = head;
         wf_batch_hdr h{};
-        h.status.code = (bad & 1) ? WF_ERR_INVALID_ARG : WF_ERR_CAPACITY;
+        h.status.code = bad ? WF_ERR_INVALID_ARG : WF_ERR_CAPACITY;
         h.fingerprint = p.fingerprint;
-        h.share = 1;
         *p.hdr = h;
         p.pre[0] = 0;
       }
@@ -159,32 +181,28 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesPara
   }
 
   // a request with few rows shares its prefix tiles with the others' (see batch_attn.cu)
-  const bool shared = prefix > 0 && total[4] >= 2;
+  const bool shared = prefix > 0 && sum_small(total) >= 2;
   for (int b = b0; b < b1; ++b) {
-    const int32_t c = p.cached[b], f = p.fresh[b];
-    const int32_t h = p.held ? p.held[b] : ceil_shift(c, p.page_shift);
+    const int32_t c = __ldg(p.cached + b), f = __ldg(p.fresh + b);
+    const int32_t h = p.held ? __ldg(p.held + b) : ceil_shift(c, p.page_shift);
     const int32_t n = max(h, ceil_shift(int64_t(c) + f, p.page_shift));
-    const int32_t tiles = (f + Tt - 1) / Tt;
-    s_start[b] = int32_t(v[0]);
-    s_first[b] = int32_t(v[1]);
-    s_ctok[b] = int32_t(v[2]);
-    s_unit[b] = int32_t(v[3]);
+    s_start[b] = int32_t(sum_tokens(v.w));
+    s_first[b] = int32_t(sum_pages(v.w));
+    s_ctok[b] = sum_ctok(v.w);
+    s_unit[b] = int32_t(sum_units(v.w));
     if (blockIdx.x == 0) {
-      p.token_start[b] = int32_t(v[0]);
+      p.token_start[b] = s_start[b];
       if (p.held_out) p.held_out[b] = n;
     }
-    v[0] += f;
-    v[1] += n - h;
-    v[2] += (tiles & 1) ? f - (tiles - 1) * Tt : 0;
-    v[3] += (tiles + 1) / 2;
+    v.add(f, n - h, Tt, p.group);
   }
-  const int32_t tokens = int32_t(total[0]);
+  const int32_t tokens = int32_t(sum_tokens(total));
   if (tid == 0) {
     s_start[p.B] = tokens;
-    s_unit[p.B] = int32_t(total[3]);
+    s_unit[p.B] = int32_t(sum_units(total));
     if (blockIdx.x == 0) {
       p.token_start[p.B] = tokens;
-      *p.free_head_out = head + int32_t(total[1]);
+      *p.free_head_out = head + int32_t(sum_pages(total));
     }
   }
   __syncthreads();
@@ -242,10 +260,10 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesPara
     r.ntok = min(pair_tokens, f - i0);
     r.pos0 = c + i0;
     r.len = c + f;
-    const int64_t last = int64_t(r.pos0) + r.ntok - 1;
-    const int64_t end = min(int64_t(r.len), (last / p.block_tokens + 1) * p.block_tokens);
+    const uint32_t last = uint32_t(r.pos0 + r.ntok - 1), G = uint32_t(p.block_tokens);
+    const int32_t end = int32_t(min(uint32_t(r.len), (last / G + 1) * G));  // the product is at most last + G
     r.ptiles = small ? -1 : ptiles;
-    r.ktiles = int32_t((end + 127) >> 7) + (small ? 0 : ptiles);
+    r.ktiles = ((end + 127) >> 7) + (small ? 0 : ptiles);
     r.cbase = r.ntok <= Tt ? s_ctok[b] : -1;
     p.units[np + u] = r;
   }
@@ -267,7 +285,7 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesPara
       if (kt > 0)
         cost[0] = (int64_t(kt) << (nt > Tt ? WF_BATCH_PAIR_SHIFT : WF_BATCH_SINGLE_SHIFT)) + WF_BATCH_UNIT_COST;
     }
-    block_scan<1>(cost, sum, scratch);
+    block_scan<1, kThreads>(cost, sum, scratch);
     if (u < np + own) p.pre[u] = carry + cost[0];
     carry += sum[0];
   }
@@ -279,15 +297,66 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesPara
     h.units = np + own;
     h.prefix_units = np;
     h.prefix_len = prefix;
-    h.ctoks = int32_t(total[2]);
+    h.ctoks = sum_ctok(total);
     h.head_cost = carry;
-    // no share is smaller than two single tiles: shorter ones cost more in merging than they save
+    // Equal shares, rounded up: a quotient in fp64, put right (64-bit divisions took 1 us of a small call).
+    // No share is smaller than two single tiles: shorter ones cost more in merging than they save.
     const int64_t all = carry * p.kv_heads;
-    h.share = max((all + p.max_ctas - 1) / p.max_ctas, int64_t(2) << WF_BATCH_SINGLE_SHIFT);
-    h.share_inv = ~uint64_t(0) / uint64_t(h.share);
-    h.ctas = int32_t((all + h.share - 1) / h.share);
+    int64_t share = int64_t(double(all) / p.max_ctas);
+    while (share * p.max_ctas < all) ++share;
+    h.share = max(share, int64_t(2) << WF_BATCH_SINGLE_SHIFT);
+    h.share_rcp = 1.0 / double(h.share);
+    int ctas = int(double(all) * h.share_rcp);
+    while (ctas > 0 && (ctas - 1) * h.share >= all) --ctas;
+    while (ctas * h.share < all) ++ctas;
+    h.ctas = ctas;
     *p.hdr = h;
   }
+}
+
+template <int kThreads>
+wf_status launch_tables(const TablesParams& p, cudaStream_t stream) {
+  const size_t smem = sizeof(int32_t) * (4 * size_t(p.B) + 2);
+  if (smem > 40 * 1024) {
+    static int attr_done[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return WF_ERR_CUDA;
+    if (dev < 0 || dev >= 64) return WF_ERR_UNSUPPORTED;
+    if (!attr_done[dev]) {
+      constexpr int kMost = int(sizeof(int32_t)) * (4 * 8192 + 2);
+      static_assert(kMost <= 220 * 1024, "lengths in shared memory");
+      if (cudaFuncSetAttribute(batch_tables_kernel<kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) !=
+          cudaSuccess) {
+        cudaGetLastError();
+        return WF_ERR_CUDA;
+      }
+      attr_done[dev] = 1;
+    }
+  }
+  const int token_blocks = (p.max_tokens + kThreads - 1) / kThreads;
+  const int most = 147 * (1024 / kThreads);
+  const int blocks = 1 + (token_blocks < most ? token_blocks : most);
+  batch_tables_kernel<kThreads><<<blocks, kThreads, smem, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
+}
+
+// SM count of the current device, asked for once per device.
+int sm_count() {
+  static int known[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (known[dev] == 0) {
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    known[dev] = sms;
+  }
+  return known[dev];
 }
 
 }  // namespace
@@ -315,10 +384,8 @@ BatchLayout batch_layout(const wf_batch_desc* d) {
     return L;
   L.ctas = d->num_ctas;
   if (L.ctas == 0) {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-      cudaGetLastError();
+    const int sms = sm_count();
+    if (sms < 1) {
       L.error = WF_ERR_CUDA;
       return L;
     }
@@ -342,7 +409,7 @@ BatchLayout batch_layout(const wf_batch_desc* d) {
   const size_t rows = size_t(L.main_rows) + size_t(L.ctas) * 4 * 128;
   L.off_lse = up(WF_ATTN_STATUS_BYTES + rows * size_t(d->head_dim) * sizeof(float));
   L.off_cuts = up(L.off_lse + rows * sizeof(float));
-  L.workspace_bytes = up(L.off_cuts + size_t(L.ctas) * 2 * sizeof(int32_t));
+  L.workspace_bytes = up(L.off_cuts + size_t(L.ctas) * WF_BATCH_CUT_BYTES);
   uint64_t f = 0xcbf29ce484222325ull;  // FNV-1a over the description's words
   const int32_t words[] = {d->num_heads, d->num_kv_heads, d->head_dim, d->dtype, d->page_tokens, d->pool_pages,
                            d->max_requests, d->max_tokens, d->max_request_pages, d->max_prefix_pages,
@@ -425,26 +492,11 @@ extern "C" wf_status wf_batch_tables(const wf_batch_desc* desc, const int32_t* c
   p.max_ctas = L.ctas;
   p.fingerprint = L.fingerprint;
 
-  const size_t smem = sizeof(int32_t) * (4 * size_t(p.B) + 2);
-  if (smem > 40 * 1024) {
-    static int attr_done[64] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return WF_ERR_CUDA;
-    if (dev < 0 || dev >= 64) return WF_ERR_UNSUPPORTED;
-    if (!attr_done[dev]) {
-      constexpr int kMost = int(sizeof(int32_t)) * (4 * 8192 + 2);
-      static_assert(kMost <= 227 * 1024 - 5 * kWarps * 8 - 16, "lengths in shared memory");
-      if (cudaFuncSetAttribute(batch_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess) {
-        cudaGetLastError();
-        return WF_ERR_CUDA;
-      }
-      attr_done[dev] = 1;
-    }
-  }
-  const int token_blocks = (p.max_tokens + kThreads - 1) / kThreads;
-  const int blocks = 1 + (token_blocks < 147 ? token_blocks : 147);
-  batch_tables_kernel<<<blocks, kThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  // Small blocks where a thread or two per request and the tokens do with
+  // them: 5 requests take 5.6 us with 256 threads a block, 7.2 us with 1024;
+  // 1024 requests 8.9 us with 1024, 10.3 us with 256.
+  return p.B <= 512 ? launch_tables<256>(p, st) : launch_tables<1024>(p, st);
 }
 
 extern "C" wf_status wf_batch_status(const void* plan, wf_stream_t stream, int32_t* detail) {

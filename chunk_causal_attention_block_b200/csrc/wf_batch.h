@@ -17,6 +17,7 @@
 #define WF_BATCH_PAIR_SHIFT 3
 #define WF_BATCH_SINGLE_SHIFT 2
 #define WF_BATCH_UNIT_COST 4
+#define WF_BATCH_CUT_BYTES 32  // workspace per CTA beside its partial rows
 
 // One work unit of the attention, for one key head: up to two 128-row tiles of
 // queries (tokens tok0 .. tok0+ntok-1, each with the key head's query heads)
@@ -44,7 +45,7 @@ struct wf_batch_hdr {
   int32_t ctoks;          // 44: tokens of one-tile units
   int64_t head_cost;      // 48: cost of one key head's units
   int64_t share;          // 56: cost of a CTA's share of all heads'
-  uint64_t share_inv;     // 64: floor((2^64 - 1) / share)
+  double share_rcp;       // 64: 1 / share
   int32_t pad[46];
 };
 

@@ -270,12 +270,11 @@ def wf_batch_workspace_bytes(desc: BatchDesc) -> int:
 def _room(where, x, n, size):
     """Address of x, which must be dense and hold n elements of `size` bytes.  Raw addresses and None pass as they are:
     their owner vouches for them."""
-    if x is None or type(x) is int:
-        return x
-    if isinstance(x, np.ndarray):
-        return x.ctypes.data
-    if x.is_contiguous() and x.itemsize == size and x.numel() >= n:
-        return x.data_ptr()
+    try:
+        if x.is_contiguous() and x.itemsize == size and x.numel() >= n:
+            return x.data_ptr()
+    except AttributeError:
+        return _ptr(x)
     raise WfError(WF_ERR_INVALID_ARG, f"{where}: {x.numel()} elements of {x.itemsize} bytes (dense: "
                                       f"{x.is_contiguous()}) where {n} of {size} are needed")
 
