@@ -135,59 +135,61 @@ struct Cfg {
 // softmax warps (8), MMA, producer, zeroing warp
 constexpr uint32_t kItemReaders = 11;
 
+// Shared memory by 32-bit addresses: two Q tiles, the K/V stages, items,
+// barriers, TMEM address, abort flag, all at fixed offsets from a 1024-aligned
+// base.  (Generic pointers cost a conversion at every use.)
+template <int D>
 struct Shared {
-  uint8_t* base;  // two Q tiles, then the K/V stages; 1024-aligned
-  uint64_t* bars;
-  uint32_t* tmem_slot;
-  int32_t* abort_flag;
-  Item* items;
+  using C = Cfg<D>;
+  static constexpr int kItemsAt = (2 + C::kStages) * C::kTile;
+  static constexpr int kBarsAt = kItemsAt + kItems * int(sizeof(Item));
+  static constexpr int kTmemAt = kBarsAt + 8 * C::kNumBars;
+  static constexpr int kAbortAt = kTmemAt + 4;
+  static_assert(kBarsAt % 8 == 0, "barrier alignment");
+
+  uint32_t base;
+
+  __device__ __forceinline__ uint32_t q_tile(int slot) const { return base + slot * C::kTile; }
+  __device__ __forceinline__ uint32_t kv_tile(int st) const { return base + (2 + st) * C::kTile; }
+  __device__ __forceinline__ uint32_t item(int it) const { return base + kItemsAt + it % kItems * int(sizeof(Item)); }
+  __device__ __forceinline__ uint32_t bar(int b) const { return base + kBarsAt + 8 * b; }
+  __device__ __forceinline__ bool aborting() const { return ld_shared_u32(base + kAbortAt) != 0; }
 };
 
-template <int D>
-__device__ __forceinline__ Shared carve_smem(uint8_t* raw) {
-  Shared s;
-  s.base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* tail = s.base + (2 + Cfg<D>::kStages) * Cfg<D>::kTile;
-  s.items = reinterpret_cast<Item*>(tail);
-  s.bars = reinterpret_cast<uint64_t*>(tail + kItems * sizeof(Item));
-  s.tmem_slot = reinterpret_cast<uint32_t*>(s.bars + Cfg<D>::kNumBars);
-  s.abort_flag = reinterpret_cast<int32_t*>(s.tmem_slot + 1);
-  return s;
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// Bounded wait; false if the CTA is aborting.  An expiry records where in one
+// 16-byte store.  Kept short: it is instantiated at every wait, and calls of
+// small items wait for the instruction cache.
 template <int D>
-__device__ __forceinline__ uint8_t* q_tile(const Shared& s, int slot) {
-  return s.base + slot * Cfg<D>::kTile;
-}
-template <int D>
-__device__ __forceinline__ uint8_t* kv_tile(const Shared& s, int st) {
-  return s.base + (2 + st) * Cfg<D>::kTile;
-}
-
-// Bounded wait; false if the CTA is aborting.  The first expiry records where.
-__device__ __forceinline__ bool wait_bar(const Shared& sh, const Params& p, int bar, uint32_t parity, int where) {
-  const uint32_t addr = smem_u32(sh.bars + bar);
+__device__ __forceinline__ bool wait_bar(const Shared<D>& sh, const Params& p, int bar, uint32_t parity, int where) {
+  const uint32_t addr = sh.bar(bar);
   if (mbar_try_wait(addr, parity)) return true;
   const uint64_t t0 = global_timer_ns();
-  for (;;) {
+  do {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (mbar_try_wait(addr, parity)) return true;
-    if (*reinterpret_cast<volatile int32_t*>(sh.abort_flag)) return false;
-    if (global_timer_ns() - t0 > p.timeout_ns) {
-      *reinterpret_cast<volatile int32_t*>(sh.abort_flag) = 1;
-      if (atomicCAS(&p.status->code, 0, int32_t(WF_ERR_DEVICE_TIMEOUT)) == 0) {
-        p.status->where = where;
-        p.status->block = int32_t(blockIdx.x);
-        p.status->thread = int32_t(threadIdx.x);
-        __threadfence();
-      }
-      return false;
-    }
-  }
+    if (sh.aborting()) return false;
+  } while (global_timer_ns() - t0 <= p.timeout_ns);
+  st_shared_u32(sh.base + Shared<D>::kAbortAt, 1);
+  *reinterpret_cast<int4*>(p.status) =
+      make_int4(WF_ERR_DEVICE_TIMEOUT, where, int32_t(blockIdx.x), int32_t(threadIdx.x));
+  return false;
 }
 
-__device__ __forceinline__ bool warp_wait(const Shared& sh, const Params& p, int bar, uint32_t parity, int where) {
+// The same without giving up for others (the end of a role): false after the limit.
+__device__ __forceinline__ bool wait_alone(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (global_timer_ns() - t0 > timeout_ns) return false;
+  return true;
+}
+
+template <int D>
+__device__ __forceinline__ bool warp_wait(const Shared<D>& sh, const Params& p, int bar, uint32_t parity, int where) {
   return __all_sync(0xffffffffu, wait_bar(sh, p, bar, parity, where));
 }
 
@@ -258,14 +260,19 @@ __device__ __forceinline__ int64_t cut_row(const Params& p, int cta, bool tail, 
 // MMA took 136 cycles to issue instead of 64 (its operands moved from ordinary
 // registers one by one).
 template <int D>
-__device__ __forceinline__ bool take_item(const Shared& sh, const Params& p, int it, Item& x, int where) {
+__device__ __forceinline__ bool take_item(const Shared<D>& sh, const Params& p, int it, Item& x, int where) {
   if (!warp_wait(sh, p, Cfg<D>::kItemFull + it % kItems, (it / kItems) & 1, where)) return false;
-  const int32_t* src = reinterpret_cast<const int32_t*>(sh.items + it % kItems);
+  const uint32_t src = sh.item(it);
   int32_t* dst = reinterpret_cast<int32_t*>(&x);
 #pragma unroll
-  for (int k = 0; k < int(sizeof(Item) / 4); ++k) dst[k] = __shfl_sync(0xffffffffu, src[k], 0);
+  for (int k = 0; k < int(sizeof(Item) / 16); ++k) {
+    uint32_t v[4];
+    ld_shared_v4(src + 16 * k, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dst[4 * k + i] = __shfl_sync(0xffffffffu, int32_t(v[i]), 0);
+  }
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(sh.bars + Cfg<D>::kItemEmpty + it % kItems));
+  if ((threadIdx.x & 31) == 0) mbar_arrive(sh.bar(Cfg<D>::kItemEmpty + it % kItems));
   return x.j1 > 0;
 }
 
@@ -276,19 +283,28 @@ __device__ __forceinline__ bool elect_one() {
   return yes != 0;
 }
 
+template <int D>
+__device__ __forceinline__ void put_item(const Shared<D>& sh, int it, const Item& x) {
+  const uint32_t dst = sh.item(it);
+  const uint32_t* src = reinterpret_cast<const uint32_t*>(&x);
+#pragma unroll
+  for (int k = 0; k < int(sizeof(Item) / 16); ++k)
+    st_shared_v4(dst + 16 * k, src[4 * k], src[4 * k + 1], src[4 * k + 2], src[4 * k + 3]);
+}
+
 __device__ __forceinline__ int32_t item_field(uint32_t item, uint32_t offset) {
   return int32_t(ld_shared_u32(item + offset));
 }
 
 // The whole warp is done with item `it`.
 template <int D>
-__device__ __forceinline__ void release_item(const Shared& sh, int it) {
+__device__ __forceinline__ void release_item(const Shared<D>& sh, int it) {
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(sh.bars + Cfg<D>::kItemEmpty + it % kItems));
+  if ((threadIdx.x & 31) == 0) mbar_arrive(sh.bar(Cfg<D>::kItemEmpty + it % kItems));
 }
 
 template <int D>
-__device__ __forceinline__ void scheduler(const Shared& sh, const Params& p) {
+__device__ __forceinline__ void scheduler(const Shared<D>& sh, const Params& p) {
   const int lane = threadIdx.x & 31;
   int it = 0;
   int32_t parity = 0;
@@ -374,8 +390,8 @@ __device__ __forceinline__ void scheduler(const Shared& sh, const Params& p) {
                    : unit_direct(r, p.tile_tokens) ? kDirect
                    : r.req < 0                     ? kMainPrefix
                                                    : kMainOwn;
-          sh.items[it % kItems] = x;
-          mbar_arrive(smem_u32(sh.bars + Cfg<D>::kItemFull + it % kItems));
+          put_item<D>(sh, it, x);
+          mbar_arrive(sh.bar(Cfg<D>::kItemFull + it % kItems));
         }
         __syncwarp();
         parity = (parity + n) & 1;
@@ -393,8 +409,8 @@ __device__ __forceinline__ void scheduler(const Shared& sh, const Params& p) {
   if (!warp_wait(sh, p, Cfg<D>::kItemEmpty + it % kItems, ((it / kItems) & 1) ^ 1, 41)) return;
   if (lane == 0) {
     Item x{};
-    sh.items[it % kItems] = x;
-    mbar_arrive(smem_u32(sh.bars + Cfg<D>::kItemFull + it % kItems));
+    put_item<D>(sh, it, x);
+    mbar_arrive(sh.bar(Cfg<D>::kItemFull + it % kItems));
   }
 }
 
@@ -444,14 +460,15 @@ __device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* t
 // shuffle and one lane issues all copies (32 lanes issuing one each serialise,
 // at about 85 cycles a copy).
 template <int D>
-__device__ __forceinline__ void load_tile(const Shared& sh, const Params& p, const CUtensorMap* tm, const KeyTile& k,
+__device__ __forceinline__ void load_tile(const Shared<D>& sh, const Params& p, const CUtensorMap* tm, const KeyTile& k,
                                           int st, int bar_index) {
   const int head = k.head_valid >> 8, valid = k.head_valid & 255;
   const int pages = (valid + (1 << p.page_shift) - 1) >> p.page_shift;
   const uint32_t page_bytes = uint32_t(Cfg<D>::kHalves * 128) << p.page_shift;
-  const uint32_t bar = smem_u32(sh.bars + bar_index);
-  uint32_t dst = smem_u32(kv_tile<D>(sh, st));
+  const uint32_t bar = sh.bar(bar_index);
+  uint32_t dst = sh.kv_tile(st);
   if (elect_one()) mbar_arrive_expect_tx(bar, uint32_t(pages) * page_bytes);
+#pragma unroll 1
   for (int pg = 0; pg < pages; ++pg, dst += page_bytes) {
     const int32_t at = __shfl_sync(0xffffffffu, k.at, pg);
     if (elect_one()) tma_load_page(dst, tm, bar, head, at);
@@ -463,7 +480,7 @@ __device__ __forceinline__ void load_tile(const Shared& sh, const Params& p, con
 // (if that subtile is the first on its tile), then the K tile of subtile m
 // (likewise).
 template <int D>
-__device__ __forceinline__ void producer(const Shared& sh, const Params& p, const CUtensorMap* tm_q,
+__device__ __forceinline__ void producer(const Shared<D>& sh, const Params& p, const CUtensorMap* tm_q,
                                          const CUtensorMap* tm_k, const CUtensorMap* tm_v) {
   using C = Cfg<D>;
   const int32_t prefix_len = p.hdr->prefix_len;
@@ -480,21 +497,22 @@ __device__ __forceinline__ void producer(const Shared& sh, const Params& p, cons
   while (ok) {
     if (more && j == x.j1) {
       more = take_item<D>(sh, p, it, x, 1);
-      if (!more && *reinterpret_cast<volatile int32_t*>(sh.abort_flag)) break;
+      if (!more && sh.aborting()) break;
       if (more) {
         ++it;
         j = x.j0;
         tiles = x.ntok > p.tile_tokens ? 2 : 1;
         next = key_tile(p, x, j, prefix_len);
+#pragma unroll 1
         for (int i = 0; i < tiles && ok; ++i, ++q_it) {
           const int slot = q_it & 1;
           if (!warp_wait(sh, p, C::kQEmpty + slot, ((q_it >> 1) & 1) ^ 1, 3)) { ok = false; break; }
-          const uint32_t bar = smem_u32(sh.bars + C::kQFull + slot);
+          const uint32_t bar = sh.bar(C::kQFull + slot);
           if (elect_one()) {
             mbar_arrive_expect_tx(bar, q_bytes);
 #pragma unroll
             for (int half = 0; half < C::kHalves; ++half)
-              tma_load_3d(smem_u32(q_tile<D>(sh, slot)) + half * kHalfBytes, tm_q, bar, 64 * half, x.head * p.group,
+              tma_load_3d(sh.q_tile(slot) + half * kHalfBytes, tm_q, bar, 64 * half, x.head * p.group,
                           x.tok0 + i * p.tile_tokens);
           }
           __syncwarp();
@@ -533,30 +551,21 @@ __device__ __forceinline__ void producer(const Shared& sh, const Params& p, cons
   }
   // The CTA must not exit with copies still landing in its shared memory: wait
   // for the last fill of every stage and Q slot, whoever gave up since.
-  for (int st = 0; st < C::kStages; ++st) {
-    if (kv_it <= st) continue;
+#pragma unroll 1
+  for (int st = 0; st < C::kStages && st < kv_it; ++st) {
     const bool raw = (raw_last >> st) & 1;
-    uint32_t parity = uint32_t((kv_it - 1 - st) / C::kStages) & 1;
-    if (raw) parity = ((raw_phase >> st) & 1) ^ 1;
-    const uint32_t addr = smem_u32(sh.bars + (raw ? C::kVRaw : C::kKVFull) + st);
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(addr, parity) && global_timer_ns() - t0 < p.timeout_ns) {
-    }
+    const uint32_t parity = raw ? ((raw_phase >> st) & 1) ^ 1 : uint32_t((kv_it - 1 - st) / C::kStages) & 1;
+    wait_alone(sh.bar((raw ? C::kVRaw : C::kKVFull) + st), parity, p.timeout_ns);
   }
-  for (int b = 0; b < 2; ++b) {
-    if (q_it <= b) continue;
-    const uint32_t parity = uint32_t((q_it - 1 - b) >> 1) & 1;
-    const uint32_t addr = smem_u32(sh.bars + C::kQFull + b);
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(addr, parity) && global_timer_ns() - t0 < p.timeout_ns) {
-    }
-  }
+#pragma unroll 1
+  for (int b = 0; b < 2 && b < q_it; ++b)
+    wait_alone(sh.bar(C::kQFull + b), uint32_t((q_it - 1 - b) >> 1) & 1, p.timeout_ns);
 }
 
 // Zero the rows behind the last key of ragged V tiles (the swizzle permutes
 // 16-byte pieces inside a row's 128 bytes only).
 template <int D>
-__device__ __forceinline__ void zero_role(const Shared& sh, const Params& p) {
+__device__ __forceinline__ void zero_role(const Shared<D>& sh, const Params& p) {
   using C = Cfg<D>;
   const int lane = threadIdx.x & 31;
   const int32_t prefix_len = p.hdr->prefix_len;
@@ -569,7 +578,7 @@ __device__ __forceinline__ void zero_role(const Shared& sh, const Params& p) {
   for (;;) {
     if (more && j == x.j1) {
       more = take_item<D>(sh, p, it, x, 51);
-      if (!more && *reinterpret_cast<volatile int32_t*>(sh.abort_flag)) return;
+      if (!more && sh.aborting()) return;
       if (more) {
         ++it;
         j = x.j0;
@@ -580,7 +589,8 @@ __device__ __forceinline__ void zero_role(const Shared& sh, const Params& p) {
       const int st = kv_it % C::kStages;
       if (!warp_wait(sh, p, C::kVRaw + st, (raw_phase >> st) & 1, 50)) return;
       raw_phase ^= 1u << st;
-      const uint32_t base = smem_u32(kv_tile<D>(sh, st)) + (lane & 7) * 16;
+      const uint32_t base = sh.kv_tile(st) + (lane & 7) * 16;
+#pragma unroll 1
       for (int row = v2 + (lane >> 3); row < 128; row += 4) {
 #pragma unroll
         for (int half = 0; half < C::kHalves; ++half)
@@ -588,7 +598,7 @@ __device__ __forceinline__ void zero_role(const Shared& sh, const Params& p) {
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(sh.bars + C::kKVFull + st));
+      if (lane == 0) mbar_arrive(sh.bar(C::kKVFull + st));
     }
     kv_it += v2 > 0;
     v2 = v1;
@@ -626,7 +636,7 @@ __device__ __forceinline__ void issue_pv_slice(uint32_t o_tmem, uint32_t p_tmem,
 constexpr uint32_t kPvLive = 1, kPvFirst = 2, kPvLast = 4, kPvOpens = 8, kPvCloses = 16;
 
 template <int D>
-__device__ __forceinline__ void mma_issuer(const Shared& sh, const Params& p, uint32_t tmem) {
+__device__ __forceinline__ void mma_issuer(const Shared<D>& sh, const Params& p, uint32_t tmem) {
   using C = Cfg<D>;
   int kv_it = 0, q_it = 0;
   uint32_t p_phase = 0;        // bit t: parity of stream t's next P
@@ -641,7 +651,7 @@ __device__ __forceinline__ void mma_issuer(const Shared& sh, const Params& p, ui
     if (more && j == n) {
       q_it += n > 0 ? tiles : 0;
       more = take_item<D>(sh, p, it, x, 10);
-      if (!more && *reinterpret_cast<volatile int32_t*>(sh.abort_flag)) break;
+      if (!more && sh.aborting()) break;
       if (more) {
         ++it;
         j = 0;
@@ -659,11 +669,11 @@ __device__ __forceinline__ void mma_issuer(const Shared& sh, const Params& p, ui
       if (!warp_wait(sh, p, C::kPFull + t, (p_phase >> t) & 1, 14 + t)) break;
       p_phase ^= 1u << t;
       tc_fence_after();
-      const uint64_t vd = smem_desc_sw128(smem_u32(kv_tile<D>(sh, vst)), kAtom, C::kGroup);
+      const uint64_t vd = smem_desc_sw128(sh.kv_tile(vst), kAtom, C::kGroup);
       if (elect_one()) {
         issue_pv_slice<D, 0>(tmem + 256 + 128 * t, tmem + 128 * t, vd, pv2 & kPvFirst ? 0u : 1u);
-        if (pv2 & kPvLast) mma_commit(smem_u32(sh.bars + C::kOFull + t));
-        if (pv2 & kPvCloses) mma_commit(smem_u32(sh.bars + C::kKVEmpty + vst));
+        if (pv2 & kPvLast) mma_commit(sh.bar(C::kOFull + t));
+        if (pv2 & kPvCloses) mma_commit(sh.bar(C::kKVEmpty + vst));
       }
       __syncwarp();
     }
@@ -681,13 +691,13 @@ __device__ __forceinline__ void mma_issuer(const Shared& sh, const Params& p, ui
     const int slot = (q_it + s) & 1;
     if (j == 0 && !warp_wait(sh, p, C::kQFull + slot, ((q_it + s) >> 1) & 1, 11)) break;
     tc_fence_after();
-    const uint64_t qd = smem_desc_sw128(smem_u32(q_tile<D>(sh, slot)), 16, kAtom);
-    const uint64_t kd = smem_desc_sw128(smem_u32(kv_tile<D>(sh, kst)), 16, C::kGroup);
+    const uint64_t qd = smem_desc_sw128(sh.q_tile(slot), 16, kAtom);
+    const uint64_t kd = smem_desc_sw128(sh.kv_tile(kst), 16, C::kGroup);
     if (elect_one()) {
       issue_s_slice<D, 0>(tmem + 128 * t, qd, kd);
-      mma_commit(smem_u32(sh.bars + C::kSFull + t));
-      if (s == tiles - 1) mma_commit(smem_u32(sh.bars + C::kKVEmpty + kst));
-      if (j == n - 1) mma_commit(smem_u32(sh.bars + C::kQEmpty + slot));
+      mma_commit(sh.bar(C::kSFull + t));
+      if (s == tiles - 1) mma_commit(sh.bar(C::kKVEmpty + kst));
+      if (j == n - 1) mma_commit(sh.bar(C::kQEmpty + slot));
     }
     __syncwarp();
     // first and last subtile of its stream in this item
@@ -700,12 +710,9 @@ __device__ __forceinline__ void mma_issuer(const Shared& sh, const Params& p, ui
     }
   }
   // all issued MMAs complete before TMEM is released
-  if (elect_one()) mma_commit(smem_u32(sh.bars + C::kMmaDone));
+  if (elect_one()) mma_commit(sh.bar(C::kMmaDone));
   __syncwarp();
-  const uint32_t addr = smem_u32(sh.bars + C::kMmaDone);
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(addr, 0) && global_timer_ns() - t0 < p.timeout_ns) {
-  }
+  wait_alone(sh.bar(C::kMmaDone), 0, p.timeout_ns);
 }
 
 // ---------------------------------------------------------------- softmax
@@ -734,7 +741,7 @@ __device__ __forceinline__ float exp_to_p(const float (&s)[128], float sl2, floa
 }
 
 template <int D>
-__device__ __forceinline__ void softmax_role(const Shared& sh, const Params& p, uint32_t tmem, int t) {
+__device__ __forceinline__ void softmax_role(const Shared<D>& sh, const Params& p, uint32_t tmem, int t) {
   using C = Cfg<D>;
   const int warp = (threadIdx.x / 32) % 4;
   const int row = warp * 32 + int(threadIdx.x & 31);
@@ -748,7 +755,7 @@ __device__ __forceinline__ void softmax_role(const Shared& sh, const Params& p, 
     // The item stays in shared memory until its epilogue is done and is read
     // again there: held in registers across the key tiles it made ptxas spill.
     if (!warp_wait(sh, p, C::kItemFull + it % kItems, (it / kItems) & 1, 20 + t)) return;
-    const uint32_t item = smem_u32(sh.items + it % kItems);
+    const uint32_t item = sh.item(it);
     const int32_t j1 = item_field(item, offsetof(Item, j1));
     if (j1 == 0) return;
     bool warp_live;
@@ -837,7 +844,7 @@ __device__ __forceinline__ void softmax_role(const Shared& sh, const Params& p, 
         tc_fence_before();
       }
       first = false;
-      mbar_arrive(smem_u32(sh.bars + C::kPFull + t));
+      mbar_arrive(sh.bar(C::kPFull + t));
     }
     // epilogue
     if (!first) {
@@ -917,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap tm_v, const Params p) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
-  const Shared sh = carve_smem<D>(smem_raw);
+  const Shared<D> sh{(smem_u32(smem_raw) + 1023) & ~1023u};
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) / 32, 0);
   const int lane = threadIdx.x % 32;
 
@@ -926,9 +933,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t count = 1;
       if (b == C::kPFull || b == C::kPFull + 1) count = 128;  // a stream's softmax threads
       if (b >= C::kItemEmpty && b < C::kItemEmpty + kItems) count = kItemReaders;
-      mbar_init(smem_u32(sh.bars + b), count);
+      mbar_init(sh.bar(b), count);
     }
-    *sh.abort_flag = 0;
+    st_shared_u32(sh.base + Shared<D>::kAbortAt, 0);
     fence_barrier_init();
     fence_proxy_async_smem();
     tma_prefetch_desc(&tm_q);
@@ -940,13 +947,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.hdr->fingerprint != p.fingerprint)
     p.status->code = WF_ERR_PLAN;  // not built, or for another description: the scheduler finds no work
   if (warp == 8) {
-    tmem_alloc(smem_u32(sh.tmem_slot), kTmemCols);
+    tmem_alloc(sh.base + Shared<D>::kTmemAt, kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *sh.tmem_slot;
+  const uint32_t tmem = ld_shared_u32(sh.base + Shared<D>::kTmemAt);
 
   if (warp < 8) {
     regs_increase<kSoftmaxRegs>();
