@@ -104,8 +104,11 @@ struct Params {
   uint64_t timeout_ns;
   float scale_log2;
   int32_t H, kv_heads, group, tile_tokens;
+  uint32_t group_inv;  // ceil(2^16 / group)
   int32_t cols, page_shift, block_tokens, max_tokens, max_ctok;
 };
+
+constexpr int kStageRows = 32 * 128;  // per softmax warp: 128 bytes of each of its rows, on their way out
 
 template <int D>
 struct Cfg {
@@ -117,7 +120,7 @@ struct Cfg {
   // 128-byte row: with 16-token pages and a copy per half, 3970 cycles for a K
   // and a V tile, where HBM delivers them in 2950.)
   static constexpr int kGroup = kHalves * kAtom;
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, 0);
   static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, 1);
   // barriers
@@ -129,19 +132,20 @@ struct Cfg {
   static constexpr int kVRaw = kKVEmpty + kStages;  // a V tile has landed whose last rows are still to be zeroed
   static constexpr int kNumBars = kVRaw + kStages;
   static constexpr int kTail = 8 * kNumBars + 16 + kItems * int(sizeof(Item));
-  static constexpr int kSmemBytes = 1024 + (2 + kStages) * kTile + (kTail + 127) / 128 * 128;
+  static constexpr int kSmemBytes = 1024 + (2 + kStages) * kTile + 8 * kStageRows + (kTail + 127) / 128 * 128;
   static_assert(kSmemBytes <= 232448, "shared memory per block");
 };
 // softmax warps (8), MMA, producer, zeroing warp
 constexpr uint32_t kItemReaders = 11;
 
-// Shared memory by 32-bit addresses: two Q tiles, the K/V stages, items,
-// barriers, TMEM address, abort flag, all at fixed offsets from a 1024-aligned
+// Shared memory by 32-bit addresses: two Q tiles, the K/V stages, outgoing
+// rows, items, barriers, TMEM address, abort flag, all at fixed offsets from a 1024-aligned
 // base.  (Generic pointers cost a conversion at every use.)
 template <int D>
 struct Shared {
   using C = Cfg<D>;
-  static constexpr int kItemsAt = (2 + C::kStages) * C::kTile;
+  static constexpr int kRowsAt = (2 + C::kStages) * C::kTile;
+  static constexpr int kItemsAt = kRowsAt + 8 * kStageRows;
   static constexpr int kBarsAt = kItemsAt + kItems * int(sizeof(Item));
   static constexpr int kTmemAt = kBarsAt + 8 * C::kNumBars;
   static constexpr int kAbortAt = kTmemAt + 4;
@@ -740,6 +744,67 @@ __device__ __forceinline__ float exp_to_p(const float (&s)[128], float sl2, floa
   return lt.x + lt.y;
 }
 
+// O * scale of the warp's 32 rows to their destinations (nullptr: none), as
+// bf16 or fp32.  A thread holds a row, but rows lie far apart in memory: stored
+// from registers, a 16-byte piece of each at a time, the two tiles of a unit
+// took 8000 cycles.  So 128 bytes of every row at a time go through shared
+// memory (the warp's own, 16-byte pieces swizzled by row) and leave as full
+// lines, eight lanes to a row.
+template <int D>
+__device__ __forceinline__ void store_rows(const Shared<D>& sh, uint32_t o_tm, uint8_t* dst, bool as_bf16, float scale) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t buf = sh.base + Shared<D>::kRowsAt + (threadIdx.x / 32) * kStageRows;
+  const uint32_t mine = buf + lane * 128;
+  const uint32_t rows = __ballot_sync(0xffffffffu, dst != nullptr);
+  const int chunks = D * (as_bf16 ? 2 : 4) / 128;
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    uint32_t r[32];
+    if (as_bf16) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        tmem_ld32(o_tm + 64 * c + 32 * h, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          uint32_t w[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            w[x] = pack_bf16x2(__uint_as_float(r[8 * v + 2 * x]) * scale, __uint_as_float(r[8 * v + 2 * x + 1]) * scale);
+          st_shared_v4(mine + (((4 * h + v) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+        }
+      }
+    } else {
+      tmem_ld32(o_tm + 32 * c, r);
+      tmem_wait_ld();
+#pragma unroll
+      for (int v = 0; v < 8; ++v) {
+#pragma unroll
+        for (int x = 4 * v; x < 4 * v + 4; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * scale);
+        st_shared_v4(mine + ((v ^ (lane & 7)) << 4), r[4 * v], r[4 * v + 1], r[4 * v + 2], r[4 * v + 3]);
+      }
+    }
+    __syncwarp();
+    // 16 rows at a time, their loads all before their stores: one warp a sub-partition hides no latency
+#pragma unroll 1
+    for (uint32_t left = rows, r0 = lane >> 3; left != 0; left >>= 16, r0 += 16) {
+      uint64_t to[4];
+      uint32_t w[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = r0 + 4 * i;
+        to[i] = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(dst), row);
+        ld_shared_v4(buf + row * 128 + (((lane & 7) ^ (row & 7)) << 4), w[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (to[i] != 0)
+          *reinterpret_cast<uint4*>(to[i] + 128 * c + (lane & 7) * 16) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+    }
+    __syncwarp();
+  }
+}
+
 template <int D>
 __device__ __forceinline__ void softmax_role(const Shared<D>& sh, const Params& p, uint32_t tmem, int t) {
   using C = Cfg<D>;
@@ -749,7 +814,7 @@ __device__ __forceinline__ void softmax_role(const Shared<D>& sh, const Params& 
   const uint32_t s_tm = tmem + lane_off + uint32_t(128 * t);
   const uint32_t o_tm = tmem + lane_off + uint32_t(256 + 128 * t);
   const int32_t prefix_len = p.hdr->prefix_len;
-  const int32_t row_tok = row / p.group;
+  const int32_t row_tok = int32_t(uint32_t(row) * p.group_inv >> 16);  // row / group, exact below 2^8
   uint32_t s_phase = 0, o_phase = 0;
   for (int it = 0;; ++it) {
     // The item stays in shared memory until its epilogue is done and is read
@@ -769,7 +834,8 @@ __device__ __forceinline__ void softmax_role(const Shared<D>& sh, const Params& 
       // own keys that this row sees
       const int32_t pos = item_field(item, offsetof(Item, pos0)) + tok_i;
       // (at most pos + block: below 2^32)
-      const uint32_t seen = (uint32_t(pos) / uint32_t(p.block_tokens) + 1) * uint32_t(p.block_tokens);
+      const uint32_t block = uint32_t(p.block_tokens);
+      const uint32_t seen = block == 1 ? uint32_t(pos) + 1 : (uint32_t(pos) / block + 1) * block;
       const uint32_t len = uint32_t(item_field(item, offsetof(Item, len)));
       limit = int32_t(seen < len ? seen : len);
       ptiles = item_field(item, offsetof(Item, ptiles));
@@ -863,58 +929,32 @@ __device__ __forceinline__ void softmax_role(const Shared<D>& sh, const Params& 
     // no key tile of this item on this stream: a direct item's rows are the other stream's
     if (!warp_live || (first && dest == kDirect)) continue;
     const bool live = row_tok < p.tile_tokens && tok_i < ntok;
-    const float inv_l = l > 0.f ? 1.0f / l : 0.f;
+    const float inv_l = l > 0.f ? __frcp_rn(l) : 0.f;
     const float lse_row = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
+    uint8_t* dst = nullptr;  // this thread's row
     if (dest == kDirect) {
-      uint4* dst = reinterpret_cast<uint4*>(p.out + (int64_t(tok) * p.H + head) * D);
-#pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {
-        uint32_t r[32];
-        tmem_ld32(o_tm + 32 * q, r);
-        tmem_wait_ld();
-        if (live) {
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            uint4 w;
-            w.x = pack_bf16x2(__uint_as_float(r[8 * v + 0]) * inv_l, __uint_as_float(r[8 * v + 1]) * inv_l);
-            w.y = pack_bf16x2(__uint_as_float(r[8 * v + 2]) * inv_l, __uint_as_float(r[8 * v + 3]) * inv_l);
-            w.z = pack_bf16x2(__uint_as_float(r[8 * v + 4]) * inv_l, __uint_as_float(r[8 * v + 5]) * inv_l);
-            w.w = pack_bf16x2(__uint_as_float(r[8 * v + 6]) * inv_l, __uint_as_float(r[8 * v + 7]) * inv_l);
-            dst[4 * q + v] = w;
-          }
-        }
+      if (live) {
+        dst = reinterpret_cast<uint8_t*>(p.out + (int64_t(tok) * p.H + head) * D);
+        if (p.lse) p.lse[int64_t(head) * p.max_tokens + tok] = lse_row;
       }
-      if (live && p.lse) p.lse[int64_t(head) * p.max_tokens + tok] = lse_row;
-      continue;
-    }
-    // partial row: normalised O and LSE
-    int64_t prow;
-    bool store = live;
-    if (dest == kMainOwn || dest == kMainPrefix) {
-      int32_t ct = cbase + tok_i;
-      if (dest == kMainPrefix) ct = live ? __ldg(p.ctok + tok) : -1;
-      store = live && ct >= 0;  // a larger request's row in a shared tile has its prefix elsewhere
-      prow = main_row(p, dest == kMainOwn, pair ? 0 : t, store ? ct : 0, head);
     } else {
-      prow = cut_row(p, int(blockIdx.x), dest == kCutTail, pair ? tile : t, row);
-    }
-    float* po = p.part_o + prow * D;
-    if (!first) {
-      float4* dst = reinterpret_cast<float4*>(po);
-#pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {
-        uint32_t r[32];
-        tmem_ld32(o_tm + 32 * q, r);
-        tmem_wait_ld();
-        if (store) {
-#pragma unroll
-          for (int v = 0; v < 8; ++v)
-            dst[8 * q + v] = make_float4(__uint_as_float(r[4 * v]) * inv_l, __uint_as_float(r[4 * v + 1]) * inv_l,
-                                         __uint_as_float(r[4 * v + 2]) * inv_l, __uint_as_float(r[4 * v + 3]) * inv_l);
-        }
+      // partial row: normalised O and LSE
+      int64_t prow;
+      bool store = live;
+      if (dest == kMainOwn || dest == kMainPrefix) {
+        int32_t ct = cbase + tok_i;
+        if (dest == kMainPrefix) ct = live ? __ldg(p.ctok + tok) : -1;
+        store = live && ct >= 0;  // a larger request's row in a shared tile has its prefix elsewhere
+        prow = main_row(p, dest == kMainOwn, pair ? 0 : t, store ? ct : 0, head);
+      } else {
+        prow = cut_row(p, int(blockIdx.x), dest == kCutTail, pair ? tile : t, row);
+      }
+      if (store) {
+        p.part_lse[prow] = lse_row;
+        if (!first) dst = reinterpret_cast<uint8_t*>(p.part_o + prow * D);
       }
     }
-    if (store) p.part_lse[prow] = lse_row;
+    if (!first) store_rows<D>(sh, o_tm, dst, dest == kDirect, inv_l);
   }
 }
 
@@ -1323,6 +1363,7 @@ extern "C" wf_status wf_batch_attn(const wf_batch_desc* desc, const void* plan, 
   p.H = desc->num_heads;
   p.kv_heads = desc->num_kv_heads;
   p.group = L.group;
+  p.group_inv = uint32_t((65536 + L.group - 1) / L.group);
   p.tile_tokens = L.tile_tokens;
   p.cols = desc->max_request_pages;
   while ((1 << p.page_shift) < desc->page_tokens) ++p.page_shift;
