@@ -87,6 +87,7 @@ static_assert(sizeof(Cut) == WF_BATCH_CUT_BYTES, "cut record layout");
 
 struct Params {
   const wf_batch_hdr* hdr;
+  const wf_batch_start* starts;
   const wf_batch_unit* units;
   const int64_t* pre;
   const int32_t* ctok;
@@ -307,39 +308,88 @@ __device__ __forceinline__ void release_item(const Shared<D>& sh, int it) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(sh.bar(Cfg<D>::kItemEmpty + it % kItems));
 }
 
+// What the scheduler reads before anything else, while the block is set up:
+// its share of the line of costs, and lane i's of the first 32 units.
+struct Share {
+  int64_t head_cost, lo, hi;
+  int32_t units, head, unit;  // units 0: nothing to do
+};
+
+__device__ __forceinline__ Share first_share(const Params& p) {
+  const wf_batch_hdr* h = p.hdr;
+  const int c = int(blockIdx.x);
+  const wf_batch_start at = p.starts[c];  // (not written if c is beyond the shares)
+  const Line line = line_of(p);
+  Share x;
+  x.head_cost = line.head_cost;
+  x.lo = share_begin(line, c);
+  x.hi = share_begin(line, c + 1);
+  x.units = h->fingerprint == p.fingerprint && x.lo < x.hi ? h->units : 0;
+  x.head = x.units > 0 ? at.head : 0;
+  x.unit = x.units > 0 ? at.unit : 0;
+  return x;
+}
+
+// A lane's unit and its cost position.
+__device__ __forceinline__ bool load_unit(const Params& p, const Share& x, int32_t head, int32_t unit, wf_batch_unit& r,
+                                          int64_t& s) {
+  if (unit >= x.units) return false;
+  const int4* src = reinterpret_cast<const int4*>(p.units + unit);
+  reinterpret_cast<int4*>(&r)[0] = __ldg(src);
+  reinterpret_cast<int4*>(&r)[1] = __ldg(src + 1);
+  s = int64_t(head) * x.head_cost + __ldg(p.pre + unit);
+  return true;
+}
+
 template <int D>
-__device__ __forceinline__ void scheduler(const Shared<D>& sh, const Params& p) {
+__device__ __forceinline__ void scheduler(const Shared<D>& sh, const Params& p, const Share& x, wf_batch_unit r,
+                                          int64_t s) {
   const int lane = threadIdx.x & 31;
   int it = 0;
   int32_t parity = 0;
-  const Line line = line_of(p);
-  const int64_t head_cost = line.head_cost;
-  const int units = p.hdr->units;
-  const int c = int(blockIdx.x);
-  const int64_t lo = share_begin(line, c), hi = share_begin(line, c + 1);
-  if (p.hdr->fingerprint == p.fingerprint && lo < hi) {
-    int32_t head = int32_t(double(lo) / double(head_cost));  // at most 255: off by one at most
-    head -= head * head_cost > lo;
-    head += (head + 1) * head_cost <= lo;
-    // first unit: the last one that starts at or before lo, found 32 probes at a time
-    const int64_t rem = lo - int64_t(head) * head_cost;
-    int32_t a = 0, b = units;
-    while (b - a > 1) {
-      const int32_t step = (b - a + 31) / 32, probe = a + lane * step;
-      const uint32_t le = __ballot_sync(0xffffffffu, probe < b && __ldg(p.pre + probe) <= rem);
-      const int k = 31 - __clz(le);  // lane 0 always holds: pre[a] <= rem
-      a = a + k * step;
-      b = min(b, a + step);
+  int32_t head = x.head, u = x.unit;
+  bool have = u + lane < x.units, more = x.units > 0, start = true;
+  while (more) {
+    // 32 units at a time, one per lane
+    int32_t j0 = 0, j1 = 0;
+    const int32_t w = tile_shift(r.ntok, p.tile_tokens);
+    if (have) share_tiles(s, w, r.ktiles, x.lo, x.hi, j0, j1);
+    more = __all_sync(0xffffffffu, !have || s < x.hi);
+    uint32_t todo = __ballot_sync(0xffffffffu, j0 < j1);
+    while (todo) {
+      const int src = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int32_t n = __shfl_sync(0xffffffffu, (j1 - j0) * (r.ntok > p.tile_tokens ? 2 : 1), src);
+      if (!warp_wait(sh, p, Cfg<D>::kItemEmpty + it % kItems, ((it / kItems) & 1) ^ 1, 40)) return;
+      if (lane == src) {
+        Item y;
+        y.j0 = j0;
+        y.j1 = j1;
+        y.head = head;
+        y.req = r.req;
+        y.tok0 = r.tok0;
+        y.ntok = r.ntok;
+        y.ptiles = r.ptiles < 0 ? 0 : r.ptiles;
+        y.cbase = r.cbase;
+        y.pos0 = r.pos0;
+        y.len = r.len;
+        y.parity = parity;
+        y.dest = j0 > 0                          ? kCutHead
+                 : j1 < r.ktiles                 ? kCutTail
+                 : unit_direct(r, p.tile_tokens) ? kDirect
+                 : r.req < 0                     ? kMainPrefix
+                                                 : kMainOwn;
+        put_item<D>(sh, it, y);
+        mbar_arrive(sh.bar(Cfg<D>::kItemFull + it % kItems));
+      }
+      __syncwarp();
+      parity = (parity + n) & 1;
+      ++it;
     }
-    int32_t u = a;
-    if (lane == 0) {
-      // for the merging, before anything is waited for
-      const wf_batch_unit r = p.units[u];
-      const int64_t s = int64_t(head) * head_cost + p.pre[u];
-      const int32_t w = tile_shift(r.ntok, p.tile_tokens);
+    if (start && lane == 0) {
+      // for the merging: whether the share begins with the first cut of a two-tile unit
+      const Line line = line_of(p);
       Cut k{};
-      int32_t j0, j1;
-      share_tiles(s, w, r.ktiles, lo, hi, j0, j1);
       if (j0 > 0 && j0 < j1 && r.req >= 0 && r.ntok > p.tile_tokens) {
         k.c0 = share_of(line, s);
         if (share_of(line, s + (int64_t(j0 - 1) << w)) == k.c0) {
@@ -351,80 +401,32 @@ __device__ __forceinline__ void scheduler(const Shared<D>& sh, const Params& p) 
           k.n = share_of(line, s + (int64_t(r.ktiles - 1) << w)) - k.c0 + 1;
         }
       }
-      p.cuts[c] = k;
+      p.cuts[blockIdx.x] = k;
     }
-    bool more = true;
-    while (more) {
-      // 32 units at a time, one per lane
-      const int32_t mine = u + lane;
-      wf_batch_unit r{};
-      int64_t s = 0;
-      if (mine < units) {
-        const int4* src = reinterpret_cast<const int4*>(p.units + mine);
-        reinterpret_cast<int4*>(&r)[0] = __ldg(src);
-        reinterpret_cast<int4*>(&r)[1] = __ldg(src + 1);
-        s = int64_t(head) * head_cost + __ldg(p.pre + mine);
-      }
-      int32_t j0 = 0, j1 = 0;
-      const int32_t w = tile_shift(r.ntok, p.tile_tokens);
-      if (mine < units) share_tiles(s, w, r.ktiles, lo, hi, j0, j1);
-      const uint32_t live = __ballot_sync(0xffffffffu, mine < units && j0 < j1);
-      more = __all_sync(0xffffffffu, mine >= units || s < hi);
-      uint32_t todo = live;
-      while (todo) {
-        const int src = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const int32_t n = __shfl_sync(0xffffffffu, (j1 - j0) * (r.ntok > p.tile_tokens ? 2 : 1), src);
-        if (!warp_wait(sh, p, Cfg<D>::kItemEmpty + it % kItems, ((it / kItems) & 1) ^ 1, 40)) return;
-        if (lane == src) {
-          Item x;
-          x.j0 = j0;
-          x.j1 = j1;
-          x.head = head;
-          x.req = r.req;
-          x.tok0 = r.tok0;
-          x.ntok = r.ntok;
-          x.ptiles = r.ptiles < 0 ? 0 : r.ptiles;
-          x.cbase = r.cbase;
-          x.pos0 = r.pos0;
-          x.len = r.len;
-          x.parity = parity;
-          x.dest = j0 > 0                          ? kCutHead
-                   : j1 < r.ktiles                 ? kCutTail
-                   : unit_direct(r, p.tile_tokens) ? kDirect
-                   : r.req < 0                     ? kMainPrefix
-                                                   : kMainOwn;
-          put_item<D>(sh, it, x);
-          mbar_arrive(sh.bar(Cfg<D>::kItemFull + it % kItems));
-        }
-        __syncwarp();
-        parity = (parity + n) & 1;
-        ++it;
-      }
-      u += 32;
-      if (u >= units) {
-        u = 0;
-        if (++head >= p.kv_heads) more = false;
-        // the next head's first unit starts where this head ends
-        if (int64_t(head) * head_cost >= hi) more = false;
-      }
+    start = false;
+    u += 32;
+    if (u >= x.units) {
+      // the next head's first unit starts where this head ends
+      u = 0;
+      ++head;
+      more = more && head < p.kv_heads && int64_t(head) * x.head_cost < x.hi;
     }
+    if (more) have = load_unit(p, x, head, u + lane, r, s);
   }
   if (!warp_wait(sh, p, Cfg<D>::kItemEmpty + it % kItems, ((it / kItems) & 1) ^ 1, 41)) return;
   if (lane == 0) {
-    Item x{};
-    put_item<D>(sh, it, x);
+    put_item<D>(sh, it, Item{});
     mbar_arrive(sh.bar(Cfg<D>::kItemFull + it % kItems));
   }
 }
 
 // ---------------------------------------------------------------- K/V tiles
-// Key tile j of an item.  Lane i of the producer holds the pool position of
+// Key tile j of an item.  Lane i of the producer holds
 // the tile's i-th page (16 at most): read from the table once, a tile ahead of
 // its use, for K and V both.
 struct KeyTile {
   int32_t head_valid;  // key head << 8 | keys (at most 128)
-  int32_t at;          // this lane's page: its first 8-token group of the pool
+  int32_t page;        // this lane's page (as loaded: used a tile later)
 };
 
 __device__ __forceinline__ int32_t tile_keys(const Item& x, int32_t j, int32_t prefix_len) {
@@ -440,12 +442,7 @@ __device__ __forceinline__ KeyTile key_tile(const Params& p, const Item& x, int3
   const int32_t pg = int32_t(threadIdx.x & 31);
   const int32_t* list = own ? p.table + x.req * p.cols : p.prefix_table;
   const int32_t first = ((own ? j - x.ptiles : j) * 128) >> p.page_shift;
-  k.at = 0;
-  if (pg << p.page_shift < valid) {
-    // an entry outside the pool reads zeros, not memory: the map's bounds hold
-    const int64_t at = int64_t(__ldg(list + first + pg)) << (p.page_shift - 3);
-    k.at = at < 0 || at > 0x0FFFFFF0 ? 0x0FFFFFF0 : int32_t(at);
-  }
+  k.page = pg << p.page_shift < valid ? __ldg(list + first + pg) : 0;
   return k;
 }
 
@@ -474,8 +471,9 @@ __device__ __forceinline__ void load_tile(const Shared<D>& sh, const Params& p, 
   if (elect_one()) mbar_arrive_expect_tx(bar, uint32_t(pages) * page_bytes);
 #pragma unroll 1
   for (int pg = 0; pg < pages; ++pg, dst += page_bytes) {
-    const int32_t at = __shfl_sync(0xffffffffu, k.at, pg);
-    if (elect_one()) tma_load_page(dst, tm, bar, head, at);
+    // in 8-token groups; an entry outside the pool reads zeros, not memory: the map's bounds hold
+    const int64_t at = int64_t(__shfl_sync(0xffffffffu, k.page, pg)) << (p.page_shift - 3);
+    if (elect_one()) tma_load_page(dst, tm, bar, head, at < 0 || at > 0x0FFFFFF0 ? 0x0FFFFFF0 : int32_t(at));
   }
 }
 
@@ -507,20 +505,6 @@ __device__ __forceinline__ void producer(const Shared<D>& sh, const Params& p, c
         j = x.j0;
         tiles = x.ntok > p.tile_tokens ? 2 : 1;
         next = key_tile(p, x, j, prefix_len);
-#pragma unroll 1
-        for (int i = 0; i < tiles && ok; ++i, ++q_it) {
-          const int slot = q_it & 1;
-          if (!warp_wait(sh, p, C::kQEmpty + slot, ((q_it >> 1) & 1) ^ 1, 3)) { ok = false; break; }
-          const uint32_t bar = sh.bar(C::kQFull + slot);
-          if (elect_one()) {
-            mbar_arrive_expect_tx(bar, q_bytes);
-#pragma unroll
-            for (int half = 0; half < C::kHalves; ++half)
-              tma_load_3d(sh.q_tile(slot) + half * kHalfBytes, tm_q, bar, 64 * half, x.head * p.group,
-                          x.tok0 + i * p.tile_tokens);
-          }
-          __syncwarp();
-        }
       }
     }
     if (more && s == 0) {
@@ -538,6 +522,25 @@ __device__ __forceinline__ void producer(const Shared<D>& sh, const Params& p, c
       raw_last = raw ? raw_last | (1u << st) : raw_last & ~(1u << st);
       if (raw) raw_phase ^= 1u << st;
       ++kv_it;
+    }
+    // An item's Q tiles follow its first K tile: their slots come free only
+    // with the last scores of the item before, and its last V tiles must not
+    // wait for that.
+    if (more && s == 0 && j == x.j0) {
+#pragma unroll 1
+      for (int i = 0; i < tiles && ok; ++i, ++q_it) {
+        const int slot = q_it & 1;
+        if (!warp_wait(sh, p, C::kQEmpty + slot, ((q_it >> 1) & 1) ^ 1, 3)) { ok = false; break; }
+        const uint32_t bar = sh.bar(C::kQFull + slot);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(bar, q_bytes);
+#pragma unroll
+          for (int half = 0; half < C::kHalves; ++half)
+            tma_load_3d(sh.q_tile(slot) + half * kHalfBytes, tm_q, bar, 64 * half, x.head * p.group,
+                        x.tok0 + i * p.tile_tokens);
+        }
+        __syncwarp();
+      }
     }
     v2 = v1;
     has2 = has1;
@@ -761,29 +764,26 @@ __device__ __forceinline__ void store_rows(const Shared<D>& sh, uint32_t o_tm, u
   for (int c = 0; c < chunks; ++c) {
     uint32_t r[32];
     if (as_bf16) {
+      uint32_t r2[32];
+      tmem_ld32(o_tm + 64 * c, r);
+      tmem_ld32(o_tm + 64 * c + 32, r2);
+      tmem_wait_ld();
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        tmem_ld32(o_tm + 64 * c + 32 * h, r);
-        tmem_wait_ld();
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          uint32_t w[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            w[x] = pack_bf16x2(__uint_as_float(r[8 * v + 2 * x]) * scale, __uint_as_float(r[8 * v + 2 * x + 1]) * scale);
-          st_shared_v4(mine + (((4 * h + v) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
-        }
+      for (int x = 0; x < 16; ++x) {
+        r[x] = pack_bf16x2(__uint_as_float(r[2 * x]) * scale, __uint_as_float(r[2 * x + 1]) * scale);
+        r2[x] = pack_bf16x2(__uint_as_float(r2[2 * x]) * scale, __uint_as_float(r2[2 * x + 1]) * scale);
       }
+#pragma unroll
+      for (int x = 0; x < 16; ++x) r[16 + x] = r2[x];
     } else {
       tmem_ld32(o_tm + 32 * c, r);
       tmem_wait_ld();
 #pragma unroll
-      for (int v = 0; v < 8; ++v) {
-#pragma unroll
-        for (int x = 4 * v; x < 4 * v + 4; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * scale);
-        st_shared_v4(mine + ((v ^ (lane & 7)) << 4), r[4 * v], r[4 * v + 1], r[4 * v + 2], r[4 * v + 3]);
-      }
+      for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * scale);
     }
+#pragma unroll
+    for (int v = 0; v < 8; ++v)
+      st_shared_v4(mine + ((v ^ (lane & 7)) << 4), r[4 * v], r[4 * v + 1], r[4 * v + 2], r[4 * v + 3]);
     __syncwarp();
     // 16 rows at a time, their loads all before their stores: one warp a sub-partition hides no latency
 #pragma unroll 1
@@ -968,19 +968,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) / 32, 0);
   const int lane = threadIdx.x % 32;
 
-  if (warp == 9 && lane == 0) {
-    for (int b = 0; b < C::kNumBars; ++b) {
+  Share share{};
+  wf_batch_unit unit{};
+  int64_t unit_at = 0;
+  if (warp == 9) {
+    for (int b = lane; b < C::kNumBars; b += 32) {
       uint32_t count = 1;
       if (b == C::kPFull || b == C::kPFull + 1) count = 128;  // a stream's softmax threads
       if (b >= C::kItemEmpty && b < C::kItemEmpty + kItems) count = kItemReaders;
       mbar_init(sh.bar(b), count);
     }
-    st_shared_u32(sh.base + Shared<D>::kAbortAt, 0);
+    if (lane == 0) st_shared_u32(sh.base + Shared<D>::kAbortAt, 0);
     fence_barrier_init();
     fence_proxy_async_smem();
-    tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+  } else if (warp == 10) {
+    share = first_share(p);
+    load_unit(p, share, share.head, share.unit + lane, unit, unit_at);
   }
   // the merging kernel may come onto this SM as soon as this block leaves it
   cudaTriggerProgrammaticLaunchCompletion();
@@ -1005,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     else if (warp == 9)
       producer<D>(sh, p, &tm_q, &tm_k, &tm_v);
     else if (warp == 10)
-      scheduler<D>(sh, p);
+      scheduler<D>(sh, p, share, unit, unit_at);
     else
       zero_role<D>(sh, p);
   }
@@ -1344,6 +1352,7 @@ extern "C" wf_status wf_batch_attn(const wf_batch_desc* desc, const void* plan, 
   const uint8_t* pl = static_cast<const uint8_t*>(plan);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.hdr = reinterpret_cast<const wf_batch_hdr*>(pl);
+  p.starts = reinterpret_cast<const wf_batch_start*>(pl + L.off_starts);
   p.units = reinterpret_cast<const wf_batch_unit*>(pl + L.off_units);
   p.pre = reinterpret_cast<const int64_t*>(pl + L.off_pre);
   p.ctok = reinterpret_cast<const int32_t*>(pl + L.off_ctok);

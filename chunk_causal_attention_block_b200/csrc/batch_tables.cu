@@ -41,6 +41,7 @@ struct TablesParams {
   int32_t* slot_map;
   int32_t* positions;
   wf_batch_hdr* hdr;
+  wf_batch_start* starts;  // [max_ctas]
   wf_batch_unit* units;
   int64_t* pre;    // exclusive sums of unit costs
   int32_t* ctok;   // partial-row index of each token, -1 for none
@@ -289,6 +290,8 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesPara
     if (u < np + own) p.pre[u] = carry + cost[0];
     carry += sum[0];
   }
+  __shared__ int64_t s_share;
+  __shared__ double s_rcp;
   if (tid == 0) {
     p.pre[np + own] = carry;
     wf_batch_hdr h{};
@@ -311,6 +314,22 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesPara
     while (ctas * h.share < all) ++ctas;
     h.ctas = ctas;
     *p.hdr = h;
+    s_share = h.share;
+    s_rcp = h.share_rcp;
+  }
+  __syncthreads();
+  // the unit that holds the beginning of each share, found from the units' side
+  const int64_t share = s_share;
+  const double rcp = s_rcp;
+  for (int u = tid; u < np + own; u += kThreads) {
+    const int64_t at = p.pre[u], end = p.pre[u + 1];
+    for (int h = 0; h < p.kv_heads; ++h) {
+      const int64_t s = h * carry + at, e = h * carry + end;
+      int c = int(double(s) * rcp);  // first share that begins at or behind s: within one of the quotient
+      while (c > 0 && (c - 1) * share >= s) --c;
+      while (c * share < s) ++c;
+      for (; c * share < e; ++c) p.starts[c] = {h, u};
+    }
   }
 }
 
@@ -399,7 +418,8 @@ BatchLayout batch_layout(const wf_batch_desc* d) {
   const int64_t ctok = int64_t(d->max_requests) * L.tile_tokens;
   L.max_ctok = ctok < d->max_tokens ? ctok : d->max_tokens;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  L.off_units = sizeof(wf_batch_hdr);
+  L.off_starts = sizeof(wf_batch_hdr);
+  L.off_units = up(L.off_starts + size_t(L.ctas) * sizeof(wf_batch_start));
   L.off_pre = up(L.off_units + size_t(L.max_units) * sizeof(wf_batch_unit));
   L.off_ctok = up(L.off_pre + size_t(L.max_units + 1) * sizeof(int64_t));
   L.off_ctok_list = up(L.off_ctok + size_t(d->max_tokens) * sizeof(int32_t));
@@ -473,6 +493,7 @@ extern "C" wf_status wf_batch_tables(const wf_batch_desc* desc, const int32_t* c
   p.positions = positions;
   uint8_t* pl = static_cast<uint8_t*>(plan);
   p.hdr = reinterpret_cast<wf_batch_hdr*>(pl);
+  p.starts = reinterpret_cast<wf_batch_start*>(pl + L.off_starts);
   p.units = reinterpret_cast<wf_batch_unit*>(pl + L.off_units);
   p.pre = reinterpret_cast<int64_t*>(pl + L.off_pre);
   p.ctok = reinterpret_cast<int32_t*>(pl + L.off_ctok);

@@ -49,6 +49,11 @@ struct wf_batch_hdr {
   int32_t pad[46];
 };
 
+// Where a CTA's share of the work begins.
+struct wf_batch_start {
+  int32_t head, unit;
+};
+
 // A token of a one-tile unit: its rows may have to be merged from parts.
 struct wf_batch_ctok {
   int32_t tok, unit;
@@ -65,7 +70,7 @@ struct BatchLayout {
   int32_t ctas;
   int32_t max_units;
   int64_t max_ctok;      // capacity of partial-row tokens
-  size_t off_units, off_pre, off_ctok, off_ctok_list, plan_bytes;
+  size_t off_starts, off_units, off_pre, off_ctok, off_ctok_list, plan_bytes;
   int64_t main_rows;     // partial rows of uncut units; those of the CTAs' cuts follow
   size_t off_cuts, off_lse, workspace_bytes;  // partial O first, after the status block
   uint64_t fingerprint;
