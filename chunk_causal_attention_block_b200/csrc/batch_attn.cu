@@ -27,7 +27,7 @@
 // is the one of attn_sm100.cu (log2 domain, reference raised only when a
 // row's maximum grows by more than 2^8).
 //
-// Warp roles (384 threads; registers as in attn_sm100.cu):
+// Warp roles (384 threads):
 //   warps 0-3, 4-7  softmax of stream 0 and 1
 //   warp  8   MMA issue (one elected lane), TMEM allocation
 //   warp  9   TMA producer: Q tiles (ring of two), K/V pages (ring of kStages)
@@ -55,8 +55,8 @@ namespace wf {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr uint32_t kSoftmaxRegs = 224;
-constexpr uint32_t kControlRegs = 56;
+constexpr uint32_t kSoftmaxRegs = 208;
+constexpr uint32_t kControlRegs = 88;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs == kThreads * 168, "register split must match launch");
 constexpr int kHalfBytes = 128 * 128;  // 64-column half of a Q tile: 128 rows x 64 bf16, 128-byte swizzled
 constexpr int kAtom = 8 * 128;         // 8 rows of 64 bf16: the swizzle's unit
@@ -107,6 +107,7 @@ struct Params {
   int32_t H, kv_heads, group, tile_tokens;
   uint32_t group_inv;  // ceil(2^16 / group)
   int32_t cols, page_shift, block_tokens, max_tokens, max_ctok;
+  int32_t stall_first_load;  // test hook: CTA 0 never issues its first K tile
 };
 
 constexpr int kStageRows = 32 * 128;  // per softmax warp: 128 bytes of each of its rows, on their way out
@@ -518,7 +519,10 @@ __device__ __forceinline__ void producer(const Shared<D>& sh, const Params& p, c
       const int st = kv_it % C::kStages;
       if (!warp_wait(sh, p, C::kKVEmpty + st, ((kv_it / C::kStages) & 1) ^ 1, 2)) { ok = false; break; }
       const bool raw = !is_k && (k.head_valid & 255) < 128;
-      load_tile<D>(sh, p, is_k ? tm_k : tm_v, k, st, raw ? C::kVRaw + st : C::kKVFull + st);
+      // failure-detection test: this fill's barrier is never armed, so that
+      // the MMA warp's bounded wait on it must expire
+      if (!(p.stall_first_load && blockIdx.x == 0 && kv_it == 0))
+        load_tile<D>(sh, p, is_k ? tm_k : tm_v, k, st, raw ? C::kVRaw + st : C::kKVFull + st);
       raw_last = raw ? raw_last | (1u << st) : raw_last & ~(1u << st);
       if (raw) raw_phase ^= 1u << st;
       ++kv_it;
@@ -1369,6 +1373,8 @@ extern "C" wf_status wf_batch_attn(const wf_batch_desc* desc, const void* plan, 
   p.fingerprint = L.fingerprint;
   p.timeout_ns = wf::wait_timeout_ns();
   p.scale_log2 = float(scale * 1.4426950408889634);
+  const char* stall = std::getenv("WF_DEBUG_STALL_FIRST_LOAD");
+  p.stall_first_load = stall && stall[0] == '1';
   p.H = desc->num_heads;
   p.kv_heads = desc->num_kv_heads;
   p.group = L.group;

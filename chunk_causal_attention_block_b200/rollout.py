@@ -17,6 +17,7 @@ import math
 from dataclasses import dataclass, field
 from typing import Optional, Sequence
 
+import numpy as np
 import torch
 
 from . import wf
@@ -275,6 +276,152 @@ class Rollout:
         self.seed = int(state["seed"])
         self.round_index = int(state["round"])
         self.stream.synchronize()
+
+
+class BranchRollout:
+    """Several continuations ("branches") of one stream's history, denoised together.
+
+    The branches start after the last round of a :class:`Rollout`: the clean
+    chunks that its next round would see become a prefix that all branches
+    share, copied once from the ring into pages of a pool; every branch then
+    runs its own wave rounds on its own pages.  One round is three calls for
+    all branches: block tables and slot map (``wf_batch_tables``), RoPE and
+    append (``wf_batch_append``) and the attention over the shared prefix
+    (``wf_batch_attn``, chunk-causal: block_tokens = C).
+
+    Branch b draws its inputs with seed + b, so branch 0 continues as the
+    parent would.  Unlike the ring, which drops a chunk per round, a branch
+    keeps all of the history it started from: for ``rounds`` rounds the window
+    grows by one chunk each.  Chunks that are denoised again keep the pages
+    they were given (``held``).  Q and K are rotated in fp32 by the plan's fp64
+    angles rounded once (the ring path rotates in fp64).
+    """
+
+    def __init__(self, parent: Rollout, branches: int, rounds: int = 1, page_tokens: int = 64, want_lse: bool = True,
+                 num_ctas: int = 0):
+        c = parent.cfg
+        if c.dtype != wf.WF_BF16 or parent.fp8:
+            raise ValueError("branches continue bf16 rollouts with 16-bit scores")
+        if branches < 1 or rounds < 1:
+            raise ValueError("at least one branch and one round")
+        self.cfg, self.parent, self.branches, self.rounds = c, parent, branches, rounds
+        self.device, self.stream, self.seed = parent.device, parent.stream, parent.seed
+        self.n0 = parent.n0_of(parent.round_index + 1)
+        self.first_tag = parent.round_index + 1
+        C, H, D, R, P = c.C, c.H, c.D, c.R, page_tokens
+        history = list(range(max(0, self.n0 - c.Wc), self.n0))
+        self.prefix_tokens = len(history) * C
+        prefix_pages = -(-self.prefix_tokens // P)
+        own_pages = -(-(rounds - 1 + R) * C // P)
+        pool_pages = prefix_pages + branches * own_pages
+        T = branches * R * C
+        kw = dict(dtype=torch.bfloat16, device=self.device)
+        i32 = dict(dtype=torch.int32, device=self.device)
+        with torch.cuda.stream(self.stream):
+            self.k_pool = torch.zeros(pool_pages * P, H, D, **kw)
+            self.v_pool = torch.zeros(pool_pages * P, H, D, **kw)
+            self.q, self.k, self.v = (torch.empty(T, H, D, **kw) for _ in range(3))
+            self.q_rot, self.out = torch.empty(T, H, D, **kw), torch.empty(T, H, D, **kw)
+            self.lse = torch.empty(H, T, dtype=torch.float32, device=self.device) if want_lse else None
+            self.rope = torch.empty(T, D // 2, 2, dtype=torch.float32, device=self.device)
+            self.slot_map, self.positions = torch.empty(max(T, C), **i32), torch.empty(max(T, C), **i32)
+            self.free_pages = torch.arange(pool_pages, **i32)
+            # in and out of a step, used in turn
+            self.free_head = [torch.zeros(1, **i32) for _ in range(2)]
+            self.held = [torch.zeros(branches, **i32) for _ in range(2)]
+            self.cached, self.fresh = torch.zeros(branches, **i32), torch.full((branches,), R * C, **i32)
+            self.prefix_len = torch.full((1,), self.prefix_tokens, **i32)
+            self.token_start = torch.empty(branches + 1, **i32)
+            self.block_table = torch.zeros(branches, own_pages, **i32)
+            self.prefix_table = torch.zeros(1, max(prefix_pages, 1), **i32)
+            self.desc = wf.make_batch_desc(H, H, D, P, pool_pages, max_requests=branches, max_tokens=T,
+                                           max_request_pages=own_pages, max_prefix_pages=prefix_pages, block_tokens=C,
+                                           num_ctas=num_ctas)
+            self.plan = torch.zeros(wf.wf_batch_plan_bytes(self.desc), dtype=torch.uint8, device=self.device)
+            self.workspace = torch.empty(wf.wf_batch_workspace_bytes(self.desc), dtype=torch.uint8, device=self.device)
+        wf.wf_attn_workspace_init(self.workspace, self.stream, nbytes=wf.WF_ATTN_STATUS_BYTES)
+        self._share_history(history, pool_pages, prefix_pages)
+        self.round_index = -1
+
+    def _share_history(self, history, pool_pages, prefix_pages):
+        """Copy the history's K'/V from the parent's ring into the prefix's pages, chunk by chunk."""
+        c, ro, P = self.cfg, self.parent, self.desc.page_tokens
+        if not history:
+            return
+        d = wf.make_batch_desc(c.H, c.H, c.D, P, pool_pages, max_requests=1, max_tokens=c.C,
+                               max_request_pages=prefix_pages, num_ctas=self.desc.num_ctas)
+        with torch.cuda.stream(self.stream):
+            plan = torch.zeros(wf.wf_batch_plan_bytes(d), dtype=torch.uint8, device=self.device)
+            fresh = torch.full((1,), c.C, dtype=torch.int32, device=self.device)
+            start = torch.empty(2, dtype=torch.int32, device=self.device)
+            for i, n in enumerate(history):
+                cached = torch.full((1,), i * c.C, dtype=torch.int32, device=self.device)
+                wf.wf_batch_tables(d, cached, fresh, None, self.free_pages, *self.free_head, self.prefix_table, start,
+                                   self.slot_map, self.positions, plan, stream=self.stream)
+                self.free_head.reverse()
+                at = slice((n % c.slots) * c.C, (n % c.slots + 1) * c.C)
+                wf.wf_batch_append(d, plan, self.slot_map, ro.k_pool[at], ro.v_pool[at], self.k_pool, self.v_pool,
+                                   stream=self.stream)
+            self.stream.synchronize()  # the step's buffers above go out of scope
+
+    def fill_inputs(self, r: int):
+        c = self.cfg
+        n = c.R * c.C
+        for b in range(self.branches):
+            for t, dst in ((wf.WF_SYNTH_Q, self.q), (wf.WF_SYNTH_K, self.k), (wf.WF_SYNTH_V, self.v)):
+                wf.wf_synth_fill(dst[b * n:(b + 1) * n], c.dtype, self.seed + b, t, self.first_tag + r, self.n0 + r, c.R,
+                                 c.C, c.H, c.D, kscale=(c.kscale and t == wf.WF_SYNTH_K), stream=self.stream)
+
+    def plan_round(self, r: int):
+        """Angles of round r's tokens, then its block tables, slot map and plan on the GPU."""
+        if not 0 <= r < self.rounds:
+            raise ValueError(f"round {r} of {self.rounds}")
+        c = self.cfg
+        with torch.cuda.stream(self.stream):
+            angles = _round_cos_sin(self.parent.desc(self.n0 + r))
+            n = c.R * c.C
+            self.rope.view(self.branches, n, c.D // 2, 2).copy_(angles.expand(self.branches, n, c.D // 2, 2))
+            self.cached.fill_(r * c.C)
+        wf.wf_batch_tables(self.desc, self.cached, self.fresh, self.prefix_len, self.free_pages, *self.free_head,
+                           self.block_table, self.token_start, self.slot_map, self.positions, self.plan,
+                           held=self.held[0], held_out=self.held[1], stream=self.stream)
+        self.free_head.reverse()
+        self.held.reverse()
+
+    def append(self):
+        wf.wf_batch_append(self.desc, self.plan, self.slot_map, self.k, self.v, self.k_pool, self.v_pool, q=self.q,
+                           rope=self.rope, q_rot=self.q_rot, stream=self.stream)
+
+    def attend(self, scale: float = 0.0):
+        wf.wf_batch_attn(self.desc, self.plan, self.block_table, self.prefix_table, self.q_rot, self.k_pool, self.v_pool,
+                         self.out, self.lse, scale, self.workspace, self.stream)
+
+    def run_round(self, r: int, fill: bool = True):
+        """Round r of every branch: inputs, tables, RoPE/append, attention.  Rounds go in order."""
+        if r != self.round_index + 1:
+            raise ValueError(f"round {r} after round {self.round_index}")
+        if fill:
+            self.fill_inputs(r)
+        self.plan_round(r)
+        self.append()
+        self.attend()
+        self.round_index = r
+
+    def device_status(self):
+        code = wf.wf_batch_status(self.plan, self.stream)
+        return (code, [code, 0, 0, 0]) if code != wf.WF_OK else wf.wf_attn_workspace_status(self.workspace, self.stream)
+
+
+def _round_cos_sin(desc: wf.RoundDesc) -> torch.Tensor:
+    """The round plan's fp64 (cos, sin) tables as one fp32 row per in-round token: [R*C, D/2, 2], on the host."""
+    host = wf.host_plan_buffer(desc)
+    wf.wf_plan_round(desc, host)
+    h = wf.decode_plan(host.numpy())
+    t, hh, ww = (torch.stack([torch.from_numpy(np.ascontiguousarray(x)) for x in h[k]], -1).float()
+                 for k in ("rope_t", "rope_h", "rope_w"))
+    frames, fh, fw = t.shape[0], hh.shape[0], ww.shape[0]
+    rows = [x.expand(frames, fh, fw, x.shape[-2], 2) for x in (t[:, None, None], hh[None, :, None], ww[None, None])]
+    return torch.cat(rows, 3).reshape(frames * fh * fw, desc.head_dim // 2, 2)
 
 
 def default_scale(cfg: RoundConfig) -> float:

@@ -16,9 +16,10 @@ class Step:
     """Buffers of one step.  The pool holds `poison` wherever no token of the step's requests or of the prefix lies."""
 
     def __init__(self, cached, fresh, prefix=0, H=4, Hkv=2, D=128, page=16, block=1, num_ctas=0, seed=0, spare_tokens=3,
-                 spare_cols=1, poison=float("nan"), held=None, scale=0.0, rope=True):
+                 spare_cols=1, poison=float("nan"), held=None, scale=0.0, rope=True, far_pages=0):
         self.cached, self.fresh, self.prefix = list(cached), list(fresh), prefix
         self.H, self.Hkv, self.D, self.page, self.block, self.scale = H, Hkv, D, page, block, scale
+        self.far_pages = far_pages
         rng = np.random.default_rng(seed)
         B, self.T = len(cached), sum(fresh)
         have = [-(-c // page) for c in cached] if held is None else list(held)
@@ -26,8 +27,9 @@ class Step:
         need = [max(h, -(-(c + f) // page)) for h, c, f in zip(have, cached, fresh)]
         cols = max(1, max(need)) + spare_cols
         pp = -(-prefix // page)
-        pool_pages = pp + sum(need) + 5
-        order = rng.permutation(pool_pages)
+        # far_pages: that many pages lie unused before the first
+        pool_pages = far_pages + pp + sum(need) + 5
+        order = far_pages + rng.permutation(pool_pages - far_pages)
         self.prefix_table = order[:pp]
         at = pp
         self.table = np.full((B, cols), -7)
@@ -131,10 +133,11 @@ class Step:
         if self.T == 0:
             return
         q = self.q if self.rope is None else self.q_rot
-        ref = orc.attention(q[:self.T].double().cpu().numpy(), self.k_pool.double().cpu().numpy(),
-                            self.v_pool.double().cpu().numpy(), self.cached, self.fresh, self.prefix,
-                            self.d["block_table"].cpu().numpy(), self.prefix_table, self.page, self.block,
-                            self.scale or None)
+        skip = self.far_pages * self.page
+        k, v = (x[skip:].double().cpu().numpy() for x in (self.k_pool, self.v_pool))
+        ref = orc.attention(q[:self.T].double().cpu().numpy(), k, v, self.cached, self.fresh, self.prefix,
+                            self.d["block_table"].cpu().numpy() - self.far_pages, self.prefix_table - self.far_pages,
+                            self.page, self.block, self.scale or None)
         out = self.out[:self.T].double().cpu().numpy()
         lse = self.lse[:, :self.T].double().cpu().numpy()
         # scores: D products added in fp32, at most a whole step each (the tensor cores may truncate)

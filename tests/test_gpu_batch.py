@@ -156,6 +156,15 @@ def test_masked_keys_may_be_anything():
         whole(cached=[1, 130, 60], fresh=[1, 1, 40], prefix=143, page=128, poison=poison)
 
 
+def test_pools_beyond_32_bit_offsets():
+    # pages at 4.3 GB and more into each pool
+    whole(cached=[100, 3], fresh=[1, 150], prefix=200, page=128, H=1, Hkv=1, far_pages=131072)
+
+
+def test_a_long_prefix_is_shared_out():
+    whole(cached=[0, 700], fresh=[1, 1], prefix=60000, H=2, Hkv=1, page=128)
+
+
 # ---------------------------------------------------------------- steps together
 def test_results_do_not_depend_on_timing():
     s = Step([900, 20, 0] * 9, [1, 1, 30] * 9, prefix=1500).run()
@@ -211,6 +220,64 @@ def test_steps_in_a_row_take_pages_one_after_another():
     s.d["positions"].fill_(-9)
     s.tables(free_head=head_in)
     s.check_tables()
+
+
+def test_two_steps_at_once_on_two_streams():
+    one, two = Step([900, 20], [1, 30], prefix=1500), Step([5, 60, 7], [200, 1, 2], prefix=300, D=64, H=6, Hkv=3)
+    for s in (one, two):
+        s.run()
+        s.check_attention()
+    outs = [s.out.clone() for s in (one, two)]
+    torch.cuda.synchronize()
+    one.stream, two.stream = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(20):
+        one.run()
+        two.run()
+    torch.cuda.synchronize()
+    for s, o in zip((one, two), outs):
+        assert torch.equal(s.out, o)
+
+
+def test_writes_stay_inside_their_buffers():
+    s = Step([20, 3, 128], [2, 300, 1], prefix=150, H=6, Hkv=3)
+    guards = []
+
+    def guard(t):
+        pad = 4096
+        raw = torch.full((t.numel() * t.element_size() + 2 * pad,), 0x5A, dtype=torch.uint8, device="cuda")
+        mid = raw[pad:pad + t.numel() * t.element_size()]
+        mid.copy_(t.contiguous().view(torch.uint8).reshape(-1))
+        guards.append((raw, pad))
+        return mid.view(t.dtype).view(t.shape)
+
+    for name in ("free_head_out", "block_table", "token_start", "slot_map", "positions", "plan"):
+        s.d[name] = guard(s.d[name])
+    for name in ("k_pool", "v_pool", "q_rot", "out", "lse", "ws"):
+        setattr(s, name, guard(getattr(s, name)))
+    s.run()
+    torch.cuda.synchronize()
+    s.check_tables()
+    s.check_attention()
+    for raw, pad in guards:
+        assert (raw[:pad] == 0x5A).all() and (raw[-pad:] == 0x5A).all()
+
+
+def test_expired_wait_reports_timeout_and_context_stays_usable(monkeypatch):
+    # CTA 0's first K tile is never loaded: every role has to leave within the limit
+    for kw in (dict(cached=[300, 20], fresh=[1, 40], prefix=700), dict(cached=[0], fresh=[900], D=64)):
+        s = Step(**kw)
+        s.tables()
+        s.append()
+        monkeypatch.setenv("WF_WAIT_TIMEOUT_MS", "100")
+        monkeypatch.setenv("WF_DEBUG_STALL_FIRST_LOAD", "1")
+        s.attend()
+        code, detail = wf.wf_attn_workspace_status(s.ws, s.stream)
+        monkeypatch.delenv("WF_DEBUG_STALL_FIRST_LOAD")
+        monkeypatch.delenv("WF_WAIT_TIMEOUT_MS")
+        assert code == wf.WF_ERR_DEVICE_TIMEOUT and detail[2] == 0, (code, detail)
+        wf.wf_attn_workspace_init(s.ws, s.stream)
+        s.attend()
+        s.check_attention()
 
 
 # ---------------------------------------------------------------- what does not fit
