@@ -64,18 +64,22 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kItems = 4;
+constexpr int kNarrow = 32;  // rows up to which an item is narrow
 
-enum Dest { kDirect = 0, kMainOwn = 1, kMainPrefix = 2, kCutHead = 3, kCutTail = 4 };
+enum Dest { kDirect = 0, kMainOwn = 1, kMainPrefix = 2, kCut = 3 };
 
 // One share of a unit for one key head, published by the scheduler.
 struct Item {
   int32_t j0, j1;   // key tiles; j1 = 0: no more items
-  int32_t head;     // key head
-  int32_t req, tok0, ntok, ptiles, cbase, pos0, len;  // of the unit (ptiles >= 0)
-  int32_t parity;   // stream of the item's first subtile
+  int32_t head;     // key head << 1 | narrow (at most kNarrow rows)
   int32_t dest;
+  int32_t req, tok0, ntok, ptiles, pos0, len;  // of the unit (ptiles >= 0)
+  int32_t parity;   // stream of the item's first subtile
+  int32_t pad;
+  int64_t row0;     // output or partial row of the item's first row (stream or row tile 0)
+  int64_t lse0;     // direct: of its LSE
 };
-static_assert(sizeof(Item) == 48, "item layout");
+static_assert(sizeof(Item) == 64, "item layout");
 
 // A two-tile unit whose first cut is the beginning of the CTA's share.
 struct Cut {
@@ -110,6 +114,7 @@ struct Params {
   int32_t stall_first_load;  // test hook: CTA 0 never issues its first K tile
 };
 
+constexpr int kXchBytes = 128 * 8;    // per stream: what its warps tell one another of narrow items' rows
 constexpr int kStageRows = 32 * 128;  // per softmax warp: 128 bytes of each of its rows, on their way out
 
 template <int D>
@@ -125,45 +130,69 @@ struct Cfg {
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, 0);
   static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, 1);
+  // narrow items: O^T = V^T P^T, A (V) MN-major, B (P) K-major
+  static constexpr uint32_t kIdescOT = idesc_bf16_f32(128, kNarrow, 0) | (1u << 15);
   // barriers
   static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6, kOFull = 8, kItemFull = 10;
   static constexpr int kItemEmpty = kItemFull + kItems;
   static constexpr int kMmaDone = kItemEmpty + kItems;
-  static constexpr int kKVFull = kMmaDone + 1;
+  static constexpr int kXch = kMmaDone + 1;  // + stream: its warps exchange row maxima or sums
+  static constexpr int kKVFull = kXch + 2;
   static constexpr int kKVEmpty = kKVFull + kStages;
   static constexpr int kVRaw = kKVEmpty + kStages;  // a V tile has landed whose last rows are still to be zeroed
   static constexpr int kNumBars = kVRaw + kStages;
-  static constexpr int kTail = 8 * kNumBars + 16 + kItems * int(sizeof(Item));
-  static constexpr int kSmemBytes = 1024 + (2 + kStages) * kTile + 8 * kStageRows + (kTail + 127) / 128 * 128;
+  // the small parts come first, then the tiles from the next 1024-byte boundary on
+  static constexpr int kSmall = kItems * int(sizeof(Item)) + 2 * kXchBytes + 8 * kNumBars + 8;
+  static constexpr int kTiles = (2 + kStages) * kTile + 8 * kStageRows;
+  static constexpr int kSmemBytes = (kSmall + 1023) / 1024 * 1024 + kTiles;
   static_assert(kSmemBytes <= 232448, "shared memory per block");
 };
 // softmax warps (8), MMA, producer, zeroing warp
 constexpr uint32_t kItemReaders = 11;
 
-// Shared memory by 32-bit addresses: two Q tiles, the K/V stages, outgoing
-// rows, items, barriers, TMEM address, abort flag, all at fixed offsets from a 1024-aligned
-// base.  (Generic pointers cost a conversion at every use.)
+// Shared memory by 32-bit addresses: items, exchange, barriers, TMEM address
+// and abort flag at `base`, two Q tiles, the K/V stages and outgoing rows at
+// `tiles`.  (Generic pointers cost a conversion at every use.)
 template <int D>
 struct Shared {
   using C = Cfg<D>;
-  static constexpr int kRowsAt = (2 + C::kStages) * C::kTile;
-  static constexpr int kItemsAt = kRowsAt + 8 * kStageRows;
-  static constexpr int kBarsAt = kItemsAt + kItems * int(sizeof(Item));
+  static constexpr int kXchAt = kItems * int(sizeof(Item));
+  static constexpr int kBarsAt = kXchAt + 2 * kXchBytes;
   static constexpr int kTmemAt = kBarsAt + 8 * C::kNumBars;
   static constexpr int kAbortAt = kTmemAt + 4;
-  static_assert(kBarsAt % 8 == 0, "barrier alignment");
+  static constexpr int kRowsAt = (2 + C::kStages) * C::kTile;
 
-  uint32_t base;
+  uint32_t base, tiles;
 
-  __device__ __forceinline__ uint32_t q_tile(int slot) const { return base + slot * C::kTile; }
-  __device__ __forceinline__ uint32_t kv_tile(int st) const { return base + (2 + st) * C::kTile; }
-  __device__ __forceinline__ uint32_t item(int it) const { return base + kItemsAt + it % kItems * int(sizeof(Item)); }
+  __device__ __forceinline__ uint32_t q_tile(int slot) const { return tiles + slot * C::kTile; }
+  __device__ __forceinline__ uint32_t kv_tile(int st) const { return tiles + (2 + st) * C::kTile; }
+  __device__ __forceinline__ uint32_t out_rows(int warp) const { return tiles + kRowsAt + warp * kStageRows; }
+  // narrow items: a stream's P (two halves of 64 keys, kNarrow rows), in its warps' outgoing rows
+  __device__ __forceinline__ uint32_t p_tile(int t) const { return tiles + kRowsAt + t * 4 * kStageRows; }
+  __device__ __forceinline__ uint32_t xch(int t) const { return base + kXchAt + t * kXchBytes; }
+  __device__ __forceinline__ uint32_t item(int it) const { return base + it % kItems * int(sizeof(Item)); }
   __device__ __forceinline__ uint32_t bar(int b) const { return base + kBarsAt + 8 * b; }
   __device__ __forceinline__ bool aborting() const { return ld_shared_u32(base + kAbortAt) != 0; }
 };
 
 __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void st_shared_f32x2(uint32_t addr, float a, float b) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
+}
+
+__device__ __forceinline__ float2 ld_shared_f32x2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ int64_t ld_shared_s64(uint32_t addr) {
+  int64_t v;
+  asm volatile("ld.shared.s64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 // Bounded wait; false if the CTA is aborting.  An expiry records where in one
@@ -301,6 +330,7 @@ __device__ __forceinline__ void put_item(const Shared<D>& sh, int it, const Item
 __device__ __forceinline__ int32_t item_field(uint32_t item, uint32_t offset) {
   return int32_t(ld_shared_u32(item + offset));
 }
+__device__ __forceinline__ int64_t item_field64(uint32_t item, uint32_t offset) { return ld_shared_s64(item + offset); }
 
 // The whole warp is done with item `it`.
 template <int D>
@@ -366,20 +396,30 @@ __device__ __forceinline__ void scheduler(const Shared<D>& sh, const Params& p, 
         Item y;
         y.j0 = j0;
         y.j1 = j1;
-        y.head = head;
+        y.head = head << 1 | (r.ntok * p.group <= kNarrow);
         y.req = r.req;
         y.tok0 = r.tok0;
         y.ntok = r.ntok;
         y.ptiles = r.ptiles < 0 ? 0 : r.ptiles;
-        y.cbase = r.cbase;
         y.pos0 = r.pos0;
         y.len = r.len;
         y.parity = parity;
-        y.dest = j0 > 0                          ? kCutHead
-                 : j1 < r.ktiles                 ? kCutTail
-                 : unit_direct(r, p.tile_tokens) ? kDirect
-                 : r.req < 0                     ? kMainPrefix
-                                                 : kMainOwn;
+        y.pad = 0;
+        const int32_t head0 = head * p.group;
+        y.lse0 = int64_t(head0) * p.max_tokens + r.tok0;
+        if (j0 > 0 || j1 < r.ktiles) {
+          y.dest = kCut;
+          y.row0 = cut_row(p, int(blockIdx.x), j0 == 0, 0, 0);
+        } else if (unit_direct(r, p.tile_tokens)) {
+          y.dest = kDirect;
+          y.row0 = int64_t(r.tok0) * p.H + head0;
+        } else if (r.req < 0) {
+          y.dest = kMainPrefix;  // the rows' tokens have partial rows of their own
+          y.row0 = head0;
+        } else {
+          y.dest = kMainOwn;
+          y.row0 = main_row(p, true, 0, r.cbase, head0);
+        }
         put_item<D>(sh, it, y);
         mbar_arrive(sh.bar(Cfg<D>::kItemFull + it % kItems));
       }
@@ -438,7 +478,7 @@ __device__ __forceinline__ int32_t tile_keys(const Item& x, int32_t j, int32_t p
 __device__ __forceinline__ KeyTile key_tile(const Params& p, const Item& x, int32_t j, int32_t prefix_len) {
   KeyTile k;
   const int32_t valid = tile_keys(x, j, prefix_len);
-  k.head_valid = x.head << 8 | valid;
+  k.head_valid = x.head >> 1 << 8 | valid;
   const bool own = j >= x.ptiles;
   const int32_t pg = int32_t(threadIdx.x & 31);
   const int32_t* list = own ? p.table + x.req * p.cols : p.prefix_table;
@@ -484,14 +524,14 @@ __device__ __forceinline__ void load_tile(const Shared<D>& sh, const Params& p, 
 // (likewise).
 template <int D>
 __device__ __forceinline__ void producer(const Shared<D>& sh, const Params& p, const CUtensorMap* tm_q,
-                                         const CUtensorMap* tm_k, const CUtensorMap* tm_v) {
+                                         const CUtensorMap* tm_narrow, const CUtensorMap* tm_k,
+                                         const CUtensorMap* tm_v) {
   using C = Cfg<D>;
   const int32_t prefix_len = p.hdr->prefix_len;
   int kv_it = 0, q_it = 0;
   uint32_t raw_phase = 0, raw_last = 0;  // per stage: parity of the next raw fill; last fill was raw
   KeyTile cur{}, next{}, v1{}, v2{};     // v1, v2: V tiles of the last and the second last subtile
   bool has1 = false, has2 = false;
-  const uint32_t q_bytes = uint32_t(p.tile_tokens * p.group) * 128 * C::kHalves;
 
   // One step per subtile, then two more for the last V tiles.
   Item x{};
@@ -536,12 +576,17 @@ __device__ __forceinline__ void producer(const Shared<D>& sh, const Params& p, c
         const int slot = q_it & 1;
         if (!warp_wait(sh, p, C::kQEmpty + slot, ((q_it >> 1) & 1) ^ 1, 3)) { ok = false; break; }
         const uint32_t bar = sh.bar(C::kQFull + slot);
+        const bool narrow = x.head & 1;
+        const CUtensorMap* tm = narrow ? tm_narrow : tm_q;
+        const int lanes = narrow ? kNarrow : 128, rows = lanes / p.group * p.group;  // a box holds the latter
         if (elect_one()) {
-          mbar_arrive_expect_tx(bar, q_bytes);
+          mbar_arrive_expect_tx(bar, uint32_t(rows * (128 / lanes)) * 128 * C::kHalves);
+#pragma unroll 1
+          for (int at = 0; at < 128; at += lanes)
 #pragma unroll
-          for (int half = 0; half < C::kHalves; ++half)
-            tma_load_3d(sh.q_tile(slot) + half * kHalfBytes, tm_q, bar, 64 * half, x.head * p.group,
-                        x.tok0 + i * p.tile_tokens);
+            for (int half = 0; half < C::kHalves; ++half)
+              tma_load_3d(sh.q_tile(slot) + half * kHalfBytes + at * 128, tm, bar, 64 * half, (x.head >> 1) * p.group,
+                          x.tok0 + i * p.tile_tokens);
         }
         __syncwarp();
       }
@@ -643,14 +688,24 @@ __device__ __forceinline__ void issue_pv_slice(uint32_t o_tmem, uint32_t p_tmem,
   if constexpr (kk < 7) issue_pv_slice<D, kk + 1>(o_tmem, p_tmem, vd, acc0);
 }
 
+// Narrow: O^T (lanes: dims, columns: rows) += V^T P^T.  With 64 dims, lanes 64
+// to 127 repeat the next 8-key group's and are not looked at.
+template <int D, int kk>
+__device__ __forceinline__ void issue_ot_slice(uint32_t o_tmem, uint64_t vd, uint64_t pd, uint32_t acc0) {
+  mma_ss_off<uint32_t((kk * 2 * Cfg<D>::kGroup) >> 4), uint32_t(((kk >> 2) * kNarrow * 128 + (kk & 3) * 32) >> 4)>(
+      o_tmem, vd, pd, Cfg<D>::kIdescOT, kk > 0 ? 1u : acc0);
+  if constexpr (kk < 7) issue_ot_slice<D, kk + 1>(o_tmem, vd, pd, acc0);
+}
+
 // What a pending PV product needs to know of its subtile.
-constexpr uint32_t kPvLive = 1, kPvFirst = 2, kPvLast = 4, kPvOpens = 8, kPvCloses = 16;
+constexpr uint32_t kPvLive = 1, kPvFirst = 2, kPvLast = 4, kPvOpens = 8, kPvCloses = 16, kPvNarrow = 32;
 
 template <int D>
 __device__ __forceinline__ void mma_issuer(const Shared<D>& sh, const Params& p, uint32_t tmem) {
   using C = Cfg<D>;
   int kv_it = 0, q_it = 0;
   uint32_t p_phase = 0;        // bit t: parity of stream t's next P
+  uint32_t ot = 0;             // bit t: which of its two O^T stream t's narrow item has
   uint32_t pv1 = 0, pv2 = 0;   // flags of the last and the second last subtile
   int vst = 0, kst = 0;
 
@@ -681,8 +736,13 @@ __device__ __forceinline__ void mma_issuer(const Shared<D>& sh, const Params& p,
       p_phase ^= 1u << t;
       tc_fence_after();
       const uint64_t vd = smem_desc_sw128(sh.kv_tile(vst), kAtom, C::kGroup);
+      if ((pv2 & kPvNarrow) && (pv2 & kPvFirst)) ot ^= 1u << t;
       if (elect_one()) {
-        issue_pv_slice<D, 0>(tmem + 256 + 128 * t, tmem + 128 * t, vd, pv2 & kPvFirst ? 0u : 1u);
+        const uint32_t acc = pv2 & kPvFirst ? 0u : 1u;
+        if (pv2 & kPvNarrow)
+          issue_ot_slice<D, 0>(tmem + 256 + 128 * t + kNarrow * ((ot >> t) & 1), vd, smem_desc_sw128(sh.p_tile(t), 16, kAtom), acc);
+        else
+          issue_pv_slice<D, 0>(tmem + 256 + 128 * t, tmem + 128 * t, vd, acc);
         if (pv2 & kPvLast) mma_commit(sh.bar(C::kOFull + t));
         if (pv2 & kPvCloses) mma_commit(sh.bar(C::kKVEmpty + vst));
       }
@@ -714,7 +774,7 @@ __device__ __forceinline__ void mma_issuer(const Shared<D>& sh, const Params& p,
     // first and last subtile of its stream in this item
     const int step = tiles == 2 ? 1 : 2;
     pv1 = kPvLive | (j < step ? kPvFirst : 0u) | (j + step >= n ? kPvLast : 0u) | (s == 0 ? kPvOpens : 0u) |
-          (s == tiles - 1 ? kPvCloses : 0u);
+          (s == tiles - 1 ? kPvCloses : 0u) | (x.head & 1 ? kPvNarrow : 0u);
     if (++s == tiles) {
       s = 0;
       ++j;
@@ -760,7 +820,7 @@ __device__ __forceinline__ float exp_to_p(const float (&s)[128], float sl2, floa
 template <int D>
 __device__ __forceinline__ void store_rows(const Shared<D>& sh, uint32_t o_tm, uint8_t* dst, bool as_bf16, float scale) {
   const int lane = threadIdx.x & 31;
-  const uint32_t buf = sh.base + Shared<D>::kRowsAt + (threadIdx.x / 32) * kStageRows;
+  const uint32_t buf = sh.out_rows(threadIdx.x / 32);
   const uint32_t mine = buf + lane * 128;
   const uint32_t rows = __ballot_sync(0xffffffffu, dst != nullptr);
   const int chunks = D * (as_bf16 ? 2 : 4) / 128;
@@ -809,53 +869,235 @@ __device__ __forceinline__ void store_rows(const Shared<D>& sh, uint32_t o_tm, u
   }
 }
 
+// The stream's four warps have all come here (and what they wrote to shared
+// memory can be read).
+template <int D>
+__device__ __forceinline__ bool stream_sync(const Shared<D>& sh, const Params& p, int t, uint32_t& phase) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(sh.bar(Cfg<D>::kXch + t));
+  const bool ok = warp_wait(sh, p, Cfg<D>::kXch + t, phase, 28 + t);
+  phase ^= 1;
+  return ok;
+}
+
+// The maximum of `a` and the sum of `b` over the stream's warps, lane by lane.
+template <int D>
+__device__ __forceinline__ bool exchange(const Shared<D>& sh, const Params& p, int t, float a, float b, float& a_max,
+                                         float& b_sum, uint32_t& phase) {
+  const uint32_t at = sh.xch(t) + (threadIdx.x & 31) * 8;
+  st_shared_f32x2(at + ((threadIdx.x >> 5) & 3) * 256, a, b);
+  if (!stream_sync<D>(sh, p, t, phase)) return false;
+  float2 v[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) v[w] = ld_shared_f32x2(at + w * 256);
+  a_max = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
+  b_sum = (v[0].y + v[1].y) + (v[2].y + v[3].y);
+  return true;
+}
+
+// One key tile of a narrow item.  Its rows stand four times in the 128 lanes
+// of S, once for each warp, which takes 32 of the tile's keys: the exp2 of few
+// rows spread over all four sub-partitions instead of 128 in a row on one
+// (2300 cycles a tile).  The warps agree on the rows' maxima, P goes to shared
+// memory as the B operand of O^T = V^T P^T, and O^T, with a dim per lane and a
+// row per column, needs no merging and leaves in coalesced stores.  Along with
+// the maxima the warps exchange `extra`, which comes back summed.
+template <int D>
+__device__ __forceinline__ bool narrow_tile(const Shared<D>& sh, const Params& p, int t, uint32_t s_tm, uint32_t o_tm,
+                                            int32_t visible, bool first, float& m_ref, float& l, float& extra,
+                                            uint32_t& x_phase) {
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+  float s[32];
+  {
+    uint32_t r[32];
+    tmem_ld32(s_tm + 32 * warp, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 32; ++c) s[c] = __uint_as_float(r[c]);
+  }
+  visible -= 32 * warp;
+  if (visible < 32) {
+    const uint32_t bits = visible <= 0 ? 0u : (1u << visible) - 1u;
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (!(bits >> c & 1)) s[c] = -INFINITY;
+  }
+  float mx[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    mx[c] = max3f(max3f(s[c], s[c + 4], s[c + 8]), max3f(s[c + 12], s[c + 16], s[c + 20]), fmaxf(s[c + 24], s[c + 28]));
+  const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+  float row_max;
+  if (!exchange<D>(sh, p, t, mine, extra, row_max, extra, x_phase)) return false;
+  const float m_new = fmaxf(m_ref, row_max);
+  if (first) {
+    m_ref = m_new;
+  } else {
+    const bool need = m_new > m_ref + kRescaleThreshold;  // the same in all four warps
+    if (__any_sync(0xffffffffu, need)) {
+      const float alpha = need ? fast_exp2(m_ref - m_new) : 1.0f;
+      uint32_t o[32];
+      tmem_ld32(o_tm, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * __shfl_sync(0xffffffffu, alpha, c));
+      tmem_st32(o_tm, o);
+      tmem_wait_st();
+      if (need) {
+        l *= alpha;
+        m_ref = m_new;
+      }
+    }
+  }
+  const float neg = m_ref == -INFINITY ? 0.f : -m_ref;  // a row that has seen no key yet: every exponent is -inf
+  const uint32_t row = sh.p_tile(t) + (warp >> 1) * (kNarrow * 128) + lane * 128;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t w[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float a = fast_exp2(fmaf(s[8 * k + 2 * x], p.scale_log2, neg));
+      const float b = fast_exp2(fmaf(s[8 * k + 2 * x + 1], p.scale_log2, neg));
+      sum[x] += a + b;
+      w[x] = pack_bf16x2(a, b);
+    }
+    st_shared_v4(row + ((((warp & 1) * 4 + k) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+  }
+  l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  fence_proxy_async_smem();  // for the tensor cores
+  return true;
+}
+
+// A narrow item's rows out of O^T: lane = dim, so a warp stores 32 dims of a
+// row at once.  dst: of the lane's row (nullptr: none); scale likewise.
+template <int D>
+__device__ __forceinline__ void store_columns(uint32_t o_tm, uint8_t* dst, bool as_bf16, float scale, int rows) {
+  const int dim = threadIdx.x & 127;
+#pragma unroll 1
+  for (int c = 0; c < rows; c += 4) {
+    uint32_t r[4];
+    tmem_ld4(o_tm + c, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint8_t* to = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(dst), c + i));
+      const float o = __uint_as_float(r[i]) * __shfl_sync(0xffffffffu, scale, c + i);
+      if (to == nullptr || dim >= D) continue;
+      if (as_bf16)
+        reinterpret_cast<__nv_bfloat16*>(to)[dim] = __float2bfloat16_rn(o);
+      else
+        reinterpret_cast<float*>(to)[dim] = o;
+    }
+  }
+}
+
+// A narrow item whose last key tile is under way.  Its rows are stored after the
+// stream's next item has handed over its first P: O^T of the two lie apart, so
+// neither the product nor the stores hold the other stream's MMAs up.
+struct Pending {
+  bool on = false;
+  float m, l;
+  int64_t row, lse;  // of the lane's row: output or partial row (-1: none), LSE
+  int32_t rows;
+  bool direct;
+};
+
+// Softmax statistics to LSE and scale of one row, and the row's destination.
+template <int D>
+__device__ __forceinline__ uint8_t* row_out(const Params& p, bool direct, int64_t row, int64_t lse, float m, float l,
+                                            bool writes_lse, bool has_o) {
+  if (row < 0) return nullptr;
+  if (writes_lse) {
+    const float x = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+    if (!direct)
+      p.part_lse[row] = x;
+    else if (p.lse)
+      p.lse[lse] = x;
+  }
+  if (!has_o) return nullptr;
+  return direct ? reinterpret_cast<uint8_t*>(p.out + row * D) : reinterpret_cast<uint8_t*>(p.part_o + row * D);
+}
+
 template <int D>
 __device__ __forceinline__ void softmax_role(const Shared<D>& sh, const Params& p, uint32_t tmem, int t) {
   using C = Cfg<D>;
   const int warp = (threadIdx.x / 32) % 4;
-  const int row = warp * 32 + int(threadIdx.x & 31);
   const uint32_t lane_off = uint32_t(warp * 32) << 16;
   const uint32_t s_tm = tmem + lane_off + uint32_t(128 * t);
   const uint32_t o_tm = tmem + lane_off + uint32_t(256 + 128 * t);
   const int32_t prefix_len = p.hdr->prefix_len;
-  const int32_t row_tok = int32_t(uint32_t(row) * p.group_inv >> 16);  // row / group, exact below 2^8
-  uint32_t s_phase = 0, o_phase = 0;
+  const int64_t half_rows = int64_t(p.max_ctok) * p.H;
+  uint32_t s_phase = 0, o_phase = 0, x_phase = 0, ot = 0;
+  Pending pend;
+  auto store_pending = [&](float sum) {
+    uint8_t* dst = row_out<D>(p, pend.direct, pend.row, pend.lse, pend.m, sum, warp == 0, true);
+    store_columns<D>(o_tm + kNarrow * (ot ^ 1), dst, pend.direct, sum > 0.f ? __frcp_rn(sum) : 0.f, pend.rows);
+    pend.on = false;
+  };
   for (int it = 0;; ++it) {
-    // The item stays in shared memory until its epilogue is done and is read
-    // again there: held in registers across the key tiles it made ptxas spill.
+    // The item stays in shared memory until its last use and is read again
+    // there: held in registers across the key tiles it made ptxas spill.
     if (!warp_wait(sh, p, C::kItemFull + it % kItems, (it / kItems) & 1, 20 + t)) return;
     const uint32_t item = sh.item(it);
     const int32_t j1 = item_field(item, offsetof(Item, j1));
+    const bool narrow = item_field(item, offsetof(Item, head)) & 1;
+    if (pend.on && !narrow) {
+      // nothing to overlap it with (the end), or an item that uses all of O
+      float none, sum;
+      if (!exchange<D>(sh, p, t, 0.f, pend.l, none, sum, x_phase)) return;
+      if (!warp_wait(sh, p, C::kOFull + t, o_phase, 24 + t)) return;
+      o_phase ^= 1;
+      tc_fence_after();
+      ot ^= 1;
+      store_pending(sum);
+      ot ^= 1;
+    }
     if (j1 == 0) return;
-    bool warp_live;
-    int32_t j, step, limit, ptiles;
+    const int32_t row = threadIdx.x & (narrow ? kNarrow - 1 : 127);
+    const int32_t row_tok = int32_t(uint32_t(row) * p.group_inv >> 16);  // row / group, exact below 2^8
+    const bool pair = item_field(item, offsetof(Item, ntok)) > p.tile_tokens;
+    const int32_t other = t ^ item_field(item, offsetof(Item, parity));
+    const int32_t tok_i = (pair && other ? p.tile_tokens : 0) + row_tok;  // token inside the unit
+    const bool live = row_tok < p.tile_tokens && tok_i < item_field(item, offsetof(Item, ntok));
+    const bool warp_live = __any_sync(0xffffffffu, live);
+    const int32_t ptiles = item_field(item, offsetof(Item, ptiles));
+    int32_t limit;  // own keys that this row sees
     {
-      const int32_t ntok = item_field(item, offsetof(Item, ntok));
-      const bool pair = ntok > p.tile_tokens;
-      const int32_t other = t ^ item_field(item, offsetof(Item, parity));
-      const int32_t tok_i = (pair && other ? p.tile_tokens : 0) + row_tok;  // token inside the unit
-      warp_live = __any_sync(0xffffffffu, row_tok < p.tile_tokens && tok_i < ntok);
-      // own keys that this row sees
-      const int32_t pos = item_field(item, offsetof(Item, pos0)) + tok_i;
-      // (at most pos + block: below 2^32)
-      const uint32_t block = uint32_t(p.block_tokens);
-      const uint32_t seen = block == 1 ? uint32_t(pos) + 1 : (uint32_t(pos) / block + 1) * block;
+      const uint32_t pos = uint32_t(item_field(item, offsetof(Item, pos0)) + tok_i), block = uint32_t(p.block_tokens);
+      const uint32_t seen = block == 1 ? pos + 1 : (pos / block + 1) * block;  // at most pos + block: below 2^32
       const uint32_t len = uint32_t(item_field(item, offsetof(Item, len)));
       limit = int32_t(seen < len ? seen : len);
-      ptiles = item_field(item, offsetof(Item, ptiles));
-      // two row tiles: every key tile for one of them; one: every second key tile
-      j = item_field(item, offsetof(Item, j0)) + (pair ? 0 : other);
-      step = pair ? 1 : 2;
     }
+    // two row tiles: every key tile for one of them; one: every second key tile
+    int32_t j = item_field(item, offsetof(Item, j0)) + (pair ? 0 : other);
+    const int32_t step = pair ? 1 : 2;
     float m_ref = -INFINITY;  // reference max (log2 units)
     float l = 0.f;
     bool first = true;
     for (; j < j1; j += step) {
       if (!warp_wait(sh, p, C::kSFull + t, s_phase, 22 + t)) return;
       s_phase ^= 1;
+      const int32_t visible = j < ptiles ? prefix_len - j * 128 : limit - (j - ptiles) * 128;
+      if (narrow) {
+        tc_fence_after();
+        if (first) ot ^= 1;
+        float sum = pend.on ? pend.l : 0.f;
+        if (!narrow_tile<D>(sh, p, t, s_tm, o_tm + kNarrow * ot, visible, first, m_ref, l, sum, x_phase)) return;
+        first = false;
+        // (before P is handed over: the item's own last product must not pass the one waited for)
+        if (pend.on) {
+          if (!warp_wait(sh, p, C::kOFull + t, o_phase, 24 + t)) return;
+          o_phase ^= 1;
+          tc_fence_after();
+        }
+        tc_fence_before();
+        mbar_arrive(sh.bar(C::kPFull + t));
+        if (pend.on) store_pending(sum);
+        continue;
+      }
       if (warp_live) {
         tc_fence_after();
-        const int32_t visible = j < ptiles ? prefix_len - j * 128 : limit - (j - ptiles) * 128;
         float s[128];
         float mxs[8];
 #pragma unroll
@@ -916,59 +1158,57 @@ __device__ __forceinline__ void softmax_role(const Shared<D>& sh, const Params& 
       first = false;
       mbar_arrive(sh.bar(C::kPFull + t));
     }
-    // epilogue
+    const int32_t dest = item_field(item, offsetof(Item, dest));
+    int64_t out_row = item_field64(item, offsetof(Item, row0)), lse = item_field64(item, offsetof(Item, lse0));
+    const int32_t rows = item_field(item, offsetof(Item, ntok)) * p.group;
+    const int32_t tok = item_field(item, offsetof(Item, tok0)) + tok_i;
+    release_item<D>(sh, it);
+    const int32_t row_head = row - row_tok * p.group;
+    lse += int64_t(row_head) * p.max_tokens + tok_i;
+    if (dest == kCut) {
+      out_row += (pair ? other : t) * 128 + row;
+    } else if (dest == kMainPrefix) {
+      const int32_t ct = live ? __ldg(p.ctok + tok) : -1;
+      // a larger request's row in a shared tile has its prefix elsewhere
+      out_row = ct < 0 ? -1 : out_row + (pair ? 0 : t * half_rows) + int64_t(ct) * p.H + row_head;
+    } else {
+      out_row += int64_t(tok_i) * p.H + row_head + (dest == kMainOwn ? t * half_rows : 0);
+    }
+    // no key tile of this item on this stream: a direct item's rows are the other stream's
+    if (!live || (first && dest == kDirect)) out_row = -1;
+    if (narrow && !first) {
+      pend.on = true;
+      pend.m = m_ref;
+      pend.l = l;
+      pend.row = out_row;
+      pend.lse = lse;
+      pend.rows = rows;
+      pend.direct = dest == kDirect;
+      continue;
+    }
     if (!first) {
       if (!warp_wait(sh, p, C::kOFull + t, o_phase, 24 + t)) return;
       o_phase ^= 1;
       tc_fence_after();
     }
-    const int32_t ntok = item_field(item, offsetof(Item, ntok)), dest = item_field(item, offsetof(Item, dest));
-    const bool pair = ntok > p.tile_tokens;
-    const int32_t tile = pair ? t ^ item_field(item, offsetof(Item, parity)) : 0;  // row tile of this stream
-    const int32_t tok_i = tile * p.tile_tokens + row_tok;
-    const int32_t head = item_field(item, offsetof(Item, head)) * p.group + (row - row_tok * p.group);
-    const int32_t tok = item_field(item, offsetof(Item, tok0)) + tok_i;
-    const int32_t cbase = item_field(item, offsetof(Item, cbase));
-    release_item<D>(sh, it);
-    // no key tile of this item on this stream: a direct item's rows are the other stream's
-    if (!warp_live || (first && dest == kDirect)) continue;
-    const bool live = row_tok < p.tile_tokens && tok_i < ntok;
-    const float inv_l = l > 0.f ? __frcp_rn(l) : 0.f;
-    const float lse_row = l > 0.f ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
-    uint8_t* dst = nullptr;  // this thread's row
-    if (dest == kDirect) {
-      if (live) {
-        dst = reinterpret_cast<uint8_t*>(p.out + (int64_t(tok) * p.H + head) * D);
-        if (p.lse) p.lse[int64_t(head) * p.max_tokens + tok] = lse_row;
-      }
-    } else {
-      // partial row: normalised O and LSE
-      int64_t prow;
-      bool store = live;
-      if (dest == kMainOwn || dest == kMainPrefix) {
-        int32_t ct = cbase + tok_i;
-        if (dest == kMainPrefix) ct = live ? __ldg(p.ctok + tok) : -1;
-        store = live && ct >= 0;  // a larger request's row in a shared tile has its prefix elsewhere
-        prow = main_row(p, dest == kMainOwn, pair ? 0 : t, store ? ct : 0, head);
-      } else {
-        prow = cut_row(p, int(blockIdx.x), dest == kCutTail, pair ? tile : t, row);
-      }
-      if (store) {
-        p.part_lse[prow] = lse_row;
-        if (!first) dst = reinterpret_cast<uint8_t*>(p.part_o + prow * D);
-      }
-    }
-    if (!first) store_rows<D>(sh, o_tm, dst, dest == kDirect, inv_l);
+    uint8_t* dst = row_out<D>(p, dest == kDirect, out_row, lse, m_ref, l, !narrow || warp == 0, !first);
+    if (!first && warp_live) store_rows<D>(sh, o_tm, dst, dest == kDirect, l > 0.f ? __frcp_rn(l) : 0.f);
   }
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    batch_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_v, const Params p) {
+    batch_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_narrow,
+                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const Params p) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
-  const Shared<D> sh{(smem_u32(smem_raw) + 1023) & ~1023u};
+  const uint32_t raw = smem_u32(smem_raw);
+  const Shared<D> sh{raw, (raw + C::kSmall + 1023) & ~1023u};
+  if (sh.tiles + C::kTiles > raw + C::kSmemBytes) {  // dynamic shared memory not on a 1024-byte boundary: never seen
+    if (threadIdx.x == 0) p.status->code = WF_ERR_ALIGNMENT;
+    return;
+  }
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) / 32, 0);
   const int lane = threadIdx.x % 32;
 
@@ -980,6 +1220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t count = 1;
       if (b == C::kPFull || b == C::kPFull + 1) count = 128;  // a stream's softmax threads
       if (b >= C::kItemEmpty && b < C::kItemEmpty + kItems) count = kItemReaders;
+      if (b == C::kXch || b == C::kXch + 1) count = 4;  // a stream's warps
       mbar_init(sh.bar(b), count);
     }
     if (lane == 0) st_shared_u32(sh.base + Shared<D>::kAbortAt, 0);
@@ -1015,7 +1256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8)
       mma_issuer<D>(sh, p, __shfl_sync(0xffffffffu, tmem, 0));
     else if (warp == 9)
-      producer<D>(sh, p, &tm_q, &tm_k, &tm_v);
+      producer<D>(sh, p, &tm_q, &tm_narrow, &tm_k, &tm_v);
     else if (warp == 10)
       scheduler<D>(sh, p, share, unit, unit_at);
     else
@@ -1297,12 +1538,14 @@ wf_status launch(const wf_batch_desc* d, const BatchLayout& L, const Params& p, 
     attr_done[dev] = 1;
   }
   const int64_t pool = int64_t(d->pool_pages) * d->page_tokens;
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tn, tk, tv;
+  // (a group of more than kNarrow heads has no narrow items)
   if (!make_q_map(&tq, q, d->max_tokens, d->num_heads, D, L.group, L.tile_tokens) ||
+      !make_q_map(&tn, q, d->max_tokens, d->num_heads, D, L.group, std::max(1, kNarrow / L.group)) ||
       !make_pool_map(&tk, k_pool, pool, d->num_kv_heads, D, d->page_tokens) ||
       !make_pool_map(&tv, v_pool, pool, d->num_kv_heads, D, d->page_tokens))
     return WF_ERR_CUDA;
-  batch_attn_kernel<D><<<L.ctas, kThreads, Cfg<D>::kSmemBytes, stream>>>(tq, tk, tv, p);
+  batch_attn_kernel<D><<<L.ctas, kThreads, Cfg<D>::kSmemBytes, stream>>>(tq, tn, tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return WF_ERR_CUDA;
   // a warp per merge_rows that can be needed, as long as they run at once
   const int64_t warps = std::max(L.max_ctok * d->num_heads, d->max_tokens > L.tile_tokens ? int64_t(L.ctas) * 64 : 0);
