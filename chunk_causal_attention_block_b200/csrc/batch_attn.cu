@@ -63,7 +63,7 @@ constexpr int kAtom = 8 * 128;         // 8 rows of 64 bf16: the swizzle's unit
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr int kItems = 4;
+constexpr int kItems = 8;
 constexpr int kNarrow = 32;  // rows up to which an item is narrow
 
 enum Dest { kDirect = 0, kMainOwn = 1, kMainPrefix = 2, kCut = 3 };
@@ -509,12 +509,22 @@ __device__ __forceinline__ void load_tile(const Shared<D>& sh, const Params& p, 
   const uint32_t page_bytes = uint32_t(Cfg<D>::kHalves * 128) << p.page_shift;
   const uint32_t bar = sh.bar(bar_index);
   uint32_t dst = sh.kv_tile(st);
+  // in 8-token groups; an entry outside the pool reads zeros, not memory: the map's bounds hold
+  const int64_t mine = int64_t(k.page) << (p.page_shift - 3);
+  const int32_t at = mine < 0 || mine > 0x0FFFFFF0 ? 0x0FFFFFF0 : int32_t(mine);
   if (elect_one()) mbar_arrive_expect_tx(bar, uint32_t(pages) * page_bytes);
+  // four pages at a time: their positions first, then the copies back to back
 #pragma unroll 1
-  for (int pg = 0; pg < pages; ++pg, dst += page_bytes) {
-    // in 8-token groups; an entry outside the pool reads zeros, not memory: the map's bounds hold
-    const int64_t at = int64_t(__shfl_sync(0xffffffffu, k.page, pg)) << (p.page_shift - 3);
-    if (elect_one()) tma_load_page(dst, tm, bar, head, at < 0 || at > 0x0FFFFFF0 ? 0x0FFFFFF0 : int32_t(at));
+  for (int pg = 0; pg < pages; pg += 4) {
+    int32_t a[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = __shfl_sync(0xffffffffu, at, pg + i);
+    if (elect_one()) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (pg + i < pages) tma_load_page(dst + i * page_bytes, tm, bar, head, a[i]);
+    }
+    dst += 4 * page_bytes;
   }
 }
 
