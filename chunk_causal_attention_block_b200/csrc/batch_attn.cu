@@ -30,13 +30,12 @@
 // Warp roles (384 threads):
 //   warps 0-3, 4-7  softmax of stream 0 and 1
 //   warp  8   MMA issue (one elected lane), TMEM allocation
-//   warp  9   TMA producer: Q tiles (ring of two), K/V pages (ring of kStages)
+//   warp  9   TMA producer of Q tiles (ring of two) and K pages
 //   warp 10   scheduler: walks this CTA's share and publishes items
-//   warp 11   zeroes the V rows behind a list's last key, whatever the page
-//             holds there (0 * NaN would reach O), before the PV MMA
+//   warp 11   TMA producer of V pages (K and V share a ring of kStages tiles)
 //
 // Every wait is bounded; on expiry the status word is set, all roles return,
-// the producer waits for its copies in flight, and TMEM is freed.
+// copies in flight are waited for, and TMEM is freed.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -75,7 +74,7 @@ struct Item {
   int32_t dest;
   int32_t req, tok0, ntok, ptiles, pos0, len;  // of the unit (ptiles >= 0)
   int32_t parity;   // stream of the item's first subtile
-  int32_t pad;
+  int32_t tile0;    // key tiles of this CTA before the item's first
   int64_t row0;     // output or partial row of the item's first row (stream or row tile 0)
   int64_t lse0;     // direct: of its LSE
 };
@@ -139,15 +138,14 @@ struct Cfg {
   static constexpr int kXch = kMmaDone + 1;  // + stream: its warps exchange row maxima or sums
   static constexpr int kKVFull = kXch + 2;
   static constexpr int kKVEmpty = kKVFull + kStages;
-  static constexpr int kVRaw = kKVEmpty + kStages;  // a V tile has landed whose last rows are still to be zeroed
-  static constexpr int kNumBars = kVRaw + kStages;
+  static constexpr int kNumBars = kKVEmpty + kStages;
   // the small parts come first, then the tiles from the next 1024-byte boundary on
-  static constexpr int kSmall = kItems * int(sizeof(Item)) + 2 * kXchBytes + 8 * kNumBars + 8;
+  static constexpr int kSmall = kItems * int(sizeof(Item)) + 2 * kXchBytes + 8 * kNumBars + 8 + 2 * kStages * 4;
   static constexpr int kTiles = (2 + kStages) * kTile + 8 * kStageRows;
   static constexpr int kSmemBytes = (kSmall + 1023) / 1024 * 1024 + kTiles;
   static_assert(kSmemBytes <= 232448, "shared memory per block");
 };
-// softmax warps (8), MMA, producer, zeroing warp
+// softmax warps (8), MMA, two producers
 constexpr uint32_t kItemReaders = 11;
 
 // Shared memory by 32-bit addresses: items, exchange, barriers, TMEM address
@@ -160,6 +158,7 @@ struct Shared {
   static constexpr int kBarsAt = kXchAt + 2 * kXchBytes;
   static constexpr int kTmemAt = kBarsAt + 8 * C::kNumBars;
   static constexpr int kAbortAt = kTmemAt + 4;
+  static constexpr int kFillsAt = kAbortAt + 4;
   static constexpr int kRowsAt = (2 + C::kStages) * C::kTile;
 
   uint32_t base, tiles;
@@ -172,6 +171,9 @@ struct Shared {
   __device__ __forceinline__ uint32_t xch(int t) const { return base + kXchAt + t * kXchBytes; }
   __device__ __forceinline__ uint32_t item(int it) const { return base + it % kItems * int(sizeof(Item)); }
   __device__ __forceinline__ uint32_t bar(int b) const { return base + kBarsAt + 8 * b; }
+  __device__ __forceinline__ uint32_t fills(int producer, int st) const {
+    return base + kFillsAt + 4 * (producer * C::kStages + st);
+  }
   __device__ __forceinline__ bool aborting() const { return ld_shared_u32(base + kAbortAt) != 0; }
 };
 
@@ -377,7 +379,7 @@ __device__ __forceinline__ void scheduler(const Shared<D>& sh, const Params& p, 
                                           int64_t s) {
   const int lane = threadIdx.x & 31;
   int it = 0;
-  int32_t parity = 0;
+  int32_t parity = 0, tile0 = 0;
   int32_t head = x.head, u = x.unit;
   bool have = u + lane < x.units, more = x.units > 0, start = true;
   while (more) {
@@ -390,7 +392,8 @@ __device__ __forceinline__ void scheduler(const Shared<D>& sh, const Params& p, 
     while (todo) {
       const int src = __ffs(todo) - 1;
       todo &= todo - 1;
-      const int32_t n = __shfl_sync(0xffffffffu, (j1 - j0) * (r.ntok > p.tile_tokens ? 2 : 1), src);
+      const int32_t n = __shfl_sync(0xffffffffu, j1 - j0, src);
+      const bool pair = __shfl_sync(0xffffffffu, r.ntok, src) > p.tile_tokens;
       if (!warp_wait(sh, p, Cfg<D>::kItemEmpty + it % kItems, ((it / kItems) & 1) ^ 1, 40)) return;
       if (lane == src) {
         Item y;
@@ -404,7 +407,7 @@ __device__ __forceinline__ void scheduler(const Shared<D>& sh, const Params& p, 
         y.pos0 = r.pos0;
         y.len = r.len;
         y.parity = parity;
-        y.pad = 0;
+        y.tile0 = tile0;
         const int32_t head0 = head * p.group;
         y.lse0 = int64_t(head0) * p.max_tokens + r.tok0;
         if (j0 > 0 || j1 < r.ktiles) {
@@ -424,7 +427,8 @@ __device__ __forceinline__ void scheduler(const Shared<D>& sh, const Params& p, 
         mbar_arrive(sh.bar(Cfg<D>::kItemFull + it % kItems));
       }
       __syncwarp();
-      parity = (parity + n) & 1;
+      parity ^= pair ? 0 : n & 1;
+      tile0 += n;
       ++it;
     }
     if (start && lane == 0) {
@@ -528,65 +532,87 @@ __device__ __forceinline__ void load_tile(const Shared<D>& sh, const Params& p, 
   }
 }
 
-// The K/V ring is filled and used in one order, which the producer, the MMA
-// thread and the zeroing warp each follow: at step m the V tile of subtile m-2
-// (if that subtile is the first on its tile), then the K tile of subtile m
-// (likewise).
+// The K/V ring is used in one order, which its two producers and the MMA warp
+// each follow: at step m the V tile of subtile m-2 (if that subtile is the
+// first on its tile), then the K tile of subtile m (likewise).  Q and K come
+// from one warp, V from another: with small pages, what a tile costs is the
+// issue of its copies.
+//
+// Subtile by subtile, with the steps of the last two V tiles at the end.
+struct Walk {
+  Item x{};
+  int it = 0, j = 0, s = 0, tiles = 1, left = 2;
+  bool more = true;
+
+  // Whether the current item is used up and another has to be taken.
+  __device__ __forceinline__ bool at_item() const { return more && j == x.j1; }
+  __device__ __forceinline__ void begin(const Params& p) {
+    ++it;
+    j = x.j0;
+    tiles = x.ntok > p.tile_tokens ? 2 : 1;
+  }
+  // Whether this step has a place for a K tile in the ring.  (The step behind a
+  // last one-row-tile subtile has, too: V tile n of the CTA then has fill 2n+2
+  // in one-tile items and 2n+1 in two-tile ones, wherever it stands.)
+  __device__ __forceinline__ bool opens_k() const { return more ? s == 0 : left == 2 && tiles == 1; }
+  // To the next subtile; false behind the last step.
+  __device__ __forceinline__ bool next() {
+    if (!more) return --left > 0;
+    if (++s == tiles) {
+      s = 0;
+      ++j;
+    }
+    return true;
+  }
+};
+
+// What a producer leaves behind for a CTA that gives up: its last fill of each stage.
 template <int D>
-__device__ __forceinline__ void producer(const Shared<D>& sh, const Params& p, const CUtensorMap* tm_q,
-                                         const CUtensorMap* tm_narrow, const CUtensorMap* tm_k,
-                                         const CUtensorMap* tm_v) {
+__device__ __forceinline__ void note_fill(const Shared<D>& sh, int producer, int st, int fill) {
+  if (elect_one()) st_shared_u32(sh.fills(producer, st), uint32_t(fill + 1));
+}
+
+template <int D>
+__device__ __forceinline__ void k_producer(const Shared<D>& sh, const Params& p, const CUtensorMap* tm_q,
+                                           const CUtensorMap* tm_narrow, const CUtensorMap* tm_k) {
   using C = Cfg<D>;
   const int32_t prefix_len = p.hdr->prefix_len;
   int kv_it = 0, q_it = 0;
-  uint32_t raw_phase = 0, raw_last = 0;  // per stage: parity of the next raw fill; last fill was raw
-  KeyTile cur{}, next{}, v1{}, v2{};     // v1, v2: V tiles of the last and the second last subtile
-  bool has1 = false, has2 = false;
-
-  // One step per subtile, then two more for the last V tiles.
-  Item x{};
-  int it = 0, j = 0, s = 0, tiles = 1, left = 2;
-  bool more = true, ok = true;
-  while (ok) {
-    if (more && j == x.j1) {
-      more = take_item<D>(sh, p, it, x, 1);
-      if (!more && sh.aborting()) break;
-      if (more) {
-        ++it;
-        j = x.j0;
-        tiles = x.ntok > p.tile_tokens ? 2 : 1;
-        next = key_tile(p, x, j, prefix_len);
-      }
+  KeyTile next{};
+  uint32_t opened = 0;  // bit 0, 1: the last and the second last subtile were the first on their tiles
+  Walk w;
+  for (;;) {
+    if (w.at_item()) {
+      w.more = take_item<D>(sh, p, w.it, w.x, 1);
+      if (!w.more) break;  // no K tile is left
+      w.begin(p);
+      next = key_tile(p, w.x, w.j, prefix_len);
     }
-    if (more && s == 0) {
-      cur = next;
-      if (j + 1 < x.j1) next = key_tile(p, x, j + 1, prefix_len);
-    }
-#pragma unroll 1
-    for (int is_k = 0; is_k < 2 && ok; ++is_k) {
-      if (is_k ? !(more && s == 0) : !has2) continue;
-      const KeyTile k = is_k ? cur : v2;
+    kv_it += (opened >> 1) & 1;  // the V tile's stage
+    if (w.s == 0) {
+      const KeyTile k = next;
+      if (w.j + 1 < w.x.j1) next = key_tile(p, w.x, w.j + 1, prefix_len);
       const int st = kv_it % C::kStages;
-      if (!warp_wait(sh, p, C::kKVEmpty + st, ((kv_it / C::kStages) & 1) ^ 1, 2)) { ok = false; break; }
-      const bool raw = !is_k && (k.head_valid & 255) < 128;
+      if (!warp_wait(sh, p, C::kKVEmpty + st, ((kv_it / C::kStages) & 1) ^ 1, 2)) break;
       // failure-detection test: this fill's barrier is never armed, so that
       // the MMA warp's bounded wait on it must expire
-      if (!(p.stall_first_load && blockIdx.x == 0 && kv_it == 0))
-        load_tile<D>(sh, p, is_k ? tm_k : tm_v, k, st, raw ? C::kVRaw + st : C::kKVFull + st);
-      raw_last = raw ? raw_last | (1u << st) : raw_last & ~(1u << st);
-      if (raw) raw_phase ^= 1u << st;
+      if (!(p.stall_first_load && blockIdx.x == 0 && kv_it == 0)) {
+        load_tile<D>(sh, p, tm_k, k, st, C::kKVFull + st);
+        note_fill(sh, 0, st, kv_it);
+      }
       ++kv_it;
     }
     // An item's Q tiles follow its first K tile: their slots come free only
-    // with the last scores of the item before, and its last V tiles must not
-    // wait for that.
-    if (more && s == 0 && j == x.j0) {
+    // with the last scores of the item before.
+    if (w.s == 0 && w.j == w.x.j0) {
+      bool ok = true;
 #pragma unroll 1
-      for (int i = 0; i < tiles && ok; ++i, ++q_it) {
+      for (int i = 0; i < w.tiles; ++i, ++q_it) {
         const int slot = q_it & 1;
-        if (!warp_wait(sh, p, C::kQEmpty + slot, ((q_it >> 1) & 1) ^ 1, 3)) { ok = false; break; }
+        ok = warp_wait(sh, p, C::kQEmpty + slot, ((q_it >> 1) & 1) ^ 1, 3);
+        if (!ok) break;
         const uint32_t bar = sh.bar(C::kQFull + slot);
-        const bool narrow = x.head & 1;
+        const bool narrow = w.x.head & 1;
         const CUtensorMap* tm = narrow ? tm_narrow : tm_q;
         const int lanes = narrow ? kNarrow : 128, rows = lanes / p.group * p.group;  // a box holds the latter
         if (elect_one()) {
@@ -595,90 +621,54 @@ __device__ __forceinline__ void producer(const Shared<D>& sh, const Params& p, c
           for (int at = 0; at < 128; at += lanes)
 #pragma unroll
             for (int half = 0; half < C::kHalves; ++half)
-              tma_load_3d(sh.q_tile(slot) + half * kHalfBytes + at * 128, tm, bar, 64 * half, (x.head >> 1) * p.group,
-                          x.tok0 + i * p.tile_tokens);
+              tma_load_3d(sh.q_tile(slot) + half * kHalfBytes + at * 128, tm, bar, 64 * half, (w.x.head >> 1) * p.group,
+                          w.x.tok0 + i * p.tile_tokens);
         }
         __syncwarp();
       }
+      if (!ok) break;
     }
-    v2 = v1;
-    has2 = has1;
-    if (more) {
-      v1 = cur;
-      has1 = s == 0;
-      if (++s == tiles) {
-        s = 0;
-        ++j;
-      }
-    } else {
-      has1 = false;
-      if (--left == 0) break;
-    }
+    opened = opened << 1 | (w.s == 0);
+    w.next();
   }
-  // The CTA must not exit with copies still landing in its shared memory: wait
-  // for the last fill of every stage and Q slot, whoever gave up since.
+  // Copies in flight end before the CTA does: by their use, or here if it gives up.
+  if (sh.aborting())
 #pragma unroll 1
-  for (int st = 0; st < C::kStages && st < kv_it; ++st) {
-    const bool raw = (raw_last >> st) & 1;
-    const uint32_t parity = raw ? ((raw_phase >> st) & 1) ^ 1 : uint32_t((kv_it - 1 - st) / C::kStages) & 1;
-    wait_alone(sh.bar((raw ? C::kVRaw : C::kKVFull) + st), parity, p.timeout_ns);
-  }
-#pragma unroll 1
-  for (int b = 0; b < 2 && b < q_it; ++b)
-    wait_alone(sh.bar(C::kQFull + b), uint32_t((q_it - 1 - b) >> 1) & 1, p.timeout_ns);
+    for (int b = 0; b < 2 && b < q_it; ++b)
+      wait_alone(sh.bar(C::kQFull + b), uint32_t((q_it - 1 - b) >> 1) & 1, p.timeout_ns);
 }
 
-// Zero the rows behind the last key of ragged V tiles (the swizzle permutes
-// 16-byte pieces inside a row's 128 bytes only).
 template <int D>
-__device__ __forceinline__ void zero_role(const Shared<D>& sh, const Params& p) {
+__device__ __forceinline__ void v_producer(const Shared<D>& sh, const Params& p, const CUtensorMap* tm_v) {
   using C = Cfg<D>;
-  const int lane = threadIdx.x & 31;
   const int32_t prefix_len = p.hdr->prefix_len;
   int kv_it = 0;
-  uint32_t raw_phase = 0;
-  int32_t v1 = 0, v2 = 0;  // valid keys of the V tiles of the last two subtiles; 0: no new tile
-  Item x{};
-  int it = 0, j = 0, s = 0, tiles = 1, left = 2;
-  bool more = true;
+  KeyTile next{}, v1{}, v2{};  // of the coming, the last and the second last subtile; head_valid 0: no tile of its own
+  Walk w;
   for (;;) {
-    if (more && j == x.j1) {
-      more = take_item<D>(sh, p, it, x, 51);
-      if (!more && sh.aborting()) return;
-      if (more) {
-        ++it;
-        j = x.j0;
-        tiles = x.ntok > p.tile_tokens ? 2 : 1;
+    if (w.at_item()) {
+      w.more = take_item<D>(sh, p, w.it, w.x, 51);
+      if (!w.more && sh.aborting()) return;
+      if (w.more) {
+        w.begin(p);
+        next = key_tile(p, w.x, w.j, prefix_len);
       }
     }
-    if (v2 > 0 && v2 < 128) {
+    if (v2.head_valid != 0) {
       const int st = kv_it % C::kStages;
-      if (!warp_wait(sh, p, C::kVRaw + st, (raw_phase >> st) & 1, 50)) return;
-      raw_phase ^= 1u << st;
-      const uint32_t base = sh.kv_tile(st) + (lane & 7) * 16;
-#pragma unroll 1
-      for (int row = v2 + (lane >> 3); row < 128; row += 4) {
-#pragma unroll
-        for (int half = 0; half < C::kHalves; ++half)
-          st_shared_v4(base + (row >> 3) * C::kGroup + half * kAtom + (row & 7) * 128, 0, 0, 0, 0);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sh.bar(C::kKVFull + st));
+      if (!warp_wait(sh, p, C::kKVEmpty + st, ((kv_it / C::kStages) & 1) ^ 1, 4)) return;
+      load_tile<D>(sh, p, tm_v, v2, st, C::kKVFull + st);
+      note_fill(sh, 1, st, kv_it);
+      ++kv_it;
     }
-    kv_it += v2 > 0;
+    kv_it += w.opens_k();
     v2 = v1;
-    if (more) {
-      kv_it += s == 0;
-      v1 = s == 0 ? tile_keys(x, j, prefix_len) : 0;
-      if (++s == tiles) {
-        s = 0;
-        ++j;
-      }
-    } else {
-      v1 = 0;
-      if (--left == 0) return;
+    v1 = KeyTile{};
+    if (w.more && w.s == 0) {
+      v1 = next;
+      if (w.j + 1 < w.x.j1) next = key_tile(p, w.x, w.j + 1, prefix_len);
     }
+    if (!w.next()) return;
   }
 }
 
@@ -760,6 +750,7 @@ __device__ __forceinline__ void mma_issuer(const Shared<D>& sh, const Params& p,
     }
     pv2 = pv1;
     if (!more) {
+      kv_it += left == 2 && tiles == 1;  // (see Walk)
       pv1 = 0;
       if (--left == 0) break;
       continue;
@@ -1002,6 +993,26 @@ __device__ __forceinline__ void store_columns(uint32_t o_tm, uint8_t* dst, bool 
   }
 }
 
+// Zeroes the rows of a V tile behind its `valid` keys, whatever their page
+// holds there (0 * NaN would reach O): by the stream whose P is the first to
+// meet the tile, before it hands P over.  (The swizzle permutes 16-byte pieces
+// inside a row's 128 bytes only.)
+template <int D>
+__device__ __forceinline__ bool zero_tail(const Shared<D>& sh, const Params& p, int fill, int32_t valid) {
+  using C = Cfg<D>;
+  const int st = fill % C::kStages, th = threadIdx.x & 127;
+  if (!warp_wait(sh, p, C::kKVFull + st, (fill / C::kStages) & 1, 26)) return false;
+  const uint32_t base = sh.kv_tile(st) + (th & 7) * 16;
+#pragma unroll 1
+  for (int row = valid + (th >> 3); row < 128; row += 16) {
+#pragma unroll
+    for (int half = 0; half < C::kHalves; ++half)
+      st_shared_v4(base + (row >> 3) * C::kGroup + half * kAtom + (row & 7) * 128, 0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  return true;
+}
+
 // A narrow item whose last key tile is under way.  Its rows are stored after the
 // stream's next item has handed over its first P: O^T of the two lie apart, so
 // neither the product nor the stores hold the other stream's MMAs up.
@@ -1072,15 +1083,16 @@ __device__ __forceinline__ void softmax_role(const Shared<D>& sh, const Params& 
     const bool live = row_tok < p.tile_tokens && tok_i < item_field(item, offsetof(Item, ntok));
     const bool warp_live = __any_sync(0xffffffffu, live);
     const int32_t ptiles = item_field(item, offsetof(Item, ptiles));
+    const int32_t len = item_field(item, offsetof(Item, len));
     int32_t limit;  // own keys that this row sees
     {
       const uint32_t pos = uint32_t(item_field(item, offsetof(Item, pos0)) + tok_i), block = uint32_t(p.block_tokens);
       const uint32_t seen = block == 1 ? pos + 1 : (pos / block + 1) * block;  // at most pos + block: below 2^32
-      const uint32_t len = uint32_t(item_field(item, offsetof(Item, len)));
-      limit = int32_t(seen < len ? seen : len);
+      limit = int32_t(seen < uint32_t(len) ? seen : uint32_t(len));
     }
     // two row tiles: every key tile for one of them; one: every second key tile
-    int32_t j = item_field(item, offsetof(Item, j0)) + (pair ? 0 : other);
+    const int32_t j0 = item_field(item, offsetof(Item, j0)), tile0 = item_field(item, offsetof(Item, tile0)) - j0;
+    int32_t j = j0 + (pair ? 0 : other);
     const int32_t step = pair ? 1 : 2;
     float m_ref = -INFINITY;  // reference max (log2 units)
     float l = 0.f;
@@ -1089,12 +1101,16 @@ __device__ __forceinline__ void softmax_role(const Shared<D>& sh, const Params& 
       if (!warp_wait(sh, p, C::kSFull + t, s_phase, 22 + t)) return;
       s_phase ^= 1;
       const int32_t visible = j < ptiles ? prefix_len - j * 128 : limit - (j - ptiles) * 128;
+      const int32_t keys = j < ptiles ? visible : len - (j - ptiles) * 128;  // of the tile, behind which rows are zeroed
+      const bool ragged = keys < 128 && !(pair && other);
+      const int32_t fill = 2 * (tile0 + j) + (pair ? 1 : 2);
       if (narrow) {
         tc_fence_after();
         if (first) ot ^= 1;
         float sum = pend.on ? pend.l : 0.f;
         if (!narrow_tile<D>(sh, p, t, s_tm, o_tm + kNarrow * ot, visible, first, m_ref, l, sum, x_phase)) return;
         first = false;
+        if (ragged && !zero_tail<D>(sh, p, fill, keys)) return;
         // (before P is handed over: the item's own last product must not pass the one waited for)
         if (pend.on) {
           if (!warp_wait(sh, p, C::kOFull + t, o_phase, 24 + t)) return;
@@ -1166,6 +1182,7 @@ __device__ __forceinline__ void softmax_role(const Shared<D>& sh, const Params& 
         tc_fence_before();
       }
       first = false;
+      if (ragged && !zero_tail<D>(sh, p, fill, keys)) return;
       mbar_arrive(sh.bar(C::kPFull + t));
     }
     const int32_t dest = item_field(item, offsetof(Item, dest));
@@ -1234,6 +1251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(sh.bar(b), count);
     }
     if (lane == 0) st_shared_u32(sh.base + Shared<D>::kAbortAt, 0);
+    if (lane < 2 * C::kStages) st_shared_u32(sh.fills(0, 0) + 4 * lane, 0);
     fence_barrier_init();
     fence_proxy_async_smem();
     if (lane == 0) {
@@ -1266,14 +1284,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8)
       mma_issuer<D>(sh, p, __shfl_sync(0xffffffffu, tmem, 0));
     else if (warp == 9)
-      producer<D>(sh, p, &tm_q, &tm_narrow, &tm_k, &tm_v);
+      k_producer<D>(sh, p, &tm_q, &tm_narrow, &tm_k);
     else if (warp == 10)
       scheduler<D>(sh, p, share, unit, unit_at);
     else
-      zero_role<D>(sh, p);
+      v_producer<D>(sh, p, &tm_v);
   }
   tc_fence_before();
   __syncthreads();
+  if (sh.aborting() && warp == 9 && lane < C::kStages) {
+    const uint32_t k = ld_shared_u32(sh.fills(0, lane)), v = ld_shared_u32(sh.fills(1, lane)), last = k > v ? k : v;
+    if (last > 0) wait_alone(sh.bar(C::kKVFull + lane), ((last - 1) / C::kStages) & 1, p.timeout_ns);
+  }
   if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
