@@ -1303,12 +1303,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- merging parts
-// A warp merges up to kRows neighbouring rows that have the same parts (the
-// query heads of one token and key head, rows of a two-tile unit).  The parts,
-// in this order: the rows' own unit's shares, then (small requests) the shares
-// of the prefix unit that holds their token.  Up to 32 parts at a time: lane i
-// finds part i's first row and LSEs, the warp their maxima and weights, and the
-// O rows are then summed, D / 32 dims per lane, kRows * kAhead loads in flight.
+// Eight lanes a row, four rows a warp.  A row's parts, in this order: its own
+// unit's shares, then (requests that share the prefix) the shares of the
+// prefix unit that holds its token.  Eight parts at a time: lane i finds part
+// i's row and LSE, the eight their maximum and weights, and the O rows are then
+// summed, D / 8 dims per lane.  (A warp a row spent most of its instructions on
+// finding the parts: 690 a row, 24 us for 22500 rows.)
 struct Parts {
   int64_t s;      // cost position of the unit
   int32_t shift, ktiles;
@@ -1344,111 +1344,75 @@ __device__ __forceinline__ int64_t part_row(const Params& p, const Line& line, c
   return j0 < j1 ? cut_row(p, c, j0 == 0, half, q.row) : -1;
 }
 
-template <int V>
-__device__ __forceinline__ void load_part(float (&o)[V], const float* row, int lane) {
-  if constexpr (V == 4) {
-    const float4 f = __ldcs(reinterpret_cast<const float4*>(row) + lane);
-    o[0] = f.x; o[1] = f.y; o[2] = f.z; o[3] = f.w;
-  } else {
-    const float2 f = __ldcs(reinterpret_cast<const float2*>(row) + lane);
-    o[0] = f.x; o[1] = f.y;
-  }
-}
-
-// ct, head0: of the first row, where parts lie by token and head; nr: rows;
-// tok, head: where each row's result goes.
-template <int D, int kRows>
-__device__ __forceinline__ void merge_rows(const Params& p, const Line& line, const Parts& a, const Parts& b, int32_t ct,
-                                           int32_t head0, int nr, const int32_t (&tok)[kRows],
-                                           const int32_t (&head)[kRows]) {
-  constexpr int V = D / 32;
-  constexpr int kAhead = kRows == 1 ? 4 : 1;
-  const int lane = threadIdx.x & 31;
-  float m[kRows], l[kRows], acc[kRows][V];
+// Merges the row of this lane's group of eight (`on`: there is one) and stores
+// it.  ct, head: where parts of uncut units lie.
+template <int D>
+__device__ __forceinline__ void merge_row(const Params& p, const Line& line, bool on, const Parts& a, const Parts& b,
+                                          int32_t ct, int32_t head, int32_t tok) {
+  constexpr int Q = D / 32;  // float4s per lane: dims 4 (g + 8 q) .. + 3
+  constexpr int kAhead = 8 / Q;
+  const int g = threadIdx.x & 7, group = threadIdx.x & 24;
+  float m = -INFINITY, l = 0.f;
+  float4 acc[Q];
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    m[r] = -INFINITY;
-    l[r] = 0.f;
-#pragma unroll
-    for (int k = 0; k < V; ++k) acc[r][k] = 0.f;
-  }
-  const int n = a.n + b.n;
-  for (int base = 0; base < n; base += 32) {
-    const int i = base + lane;
+  for (int q = 0; q < Q; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int n = on ? a.n + b.n : 0, most = __reduce_max_sync(0xffffffffu, n);
+#pragma unroll 1
+  for (int base = 0; base < most; base += 8) {
+    const int i = base + g;
     int64_t row = -1;
-    if (i < a.n)
-      row = part_row(p, line, a, i, ct, head0);
-    else if (i < n)
-      row = part_row(p, line, b, i - a.n, ct, head0);
-    float w[kRows];
+    if (i < n) row = i < a.n ? part_row(p, line, a, i, ct, head) : part_row(p, line, b, i - a.n, ct, head);
+    // (a part that saw no key has no O row: its weight is 0 and it is not read)
+    const float x = row >= 0 ? p.part_lse[row] : -INFINITY;
+    float mx = x;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) w[r] = row >= 0 && r < nr ? p.part_lse[row + r] : -INFINITY;
-    uint32_t todo = 0;  // a part that saw no key of a row has no O row: its weight is 0 and it is not read
+    for (int off = 4; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    const float m_new = fmaxf(m, mx);
+    const float old = m == -INFINITY ? 0.f : __expf(m - m_new);
+    const float w = x == -INFINITY ? 0.f : __expf(x - m_new);
+    float ws = w;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      float mx = w[r];
+    for (int off = 4; off > 0; off >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, off);
+    l = l * old + ws;
+    m = m_new;
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-      todo |= __ballot_sync(0xffffffffu, w[r] != -INFINITY);
-      const float m_new = fmaxf(m[r], mx);
-      const float old = m[r] == -INFINITY ? 0.f : expf(m[r] - m_new);
-      w[r] = w[r] == -INFINITY ? 0.f : expf(w[r] - m_new);
-      float ws = w[r];
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, off);
-      l[r] = l[r] * old + ws;
-      m[r] = m_new;
-#pragma unroll
-      for (int k = 0; k < V; ++k) acc[r][k] *= old;
+    for (int q = 0; q < Q; ++q) {
+      acc[q].x *= old; acc[q].y *= old; acc[q].z *= old; acc[q].w *= old;
     }
-    while (todo) {
-      float o[kAhead][kRows][V], wk[kAhead][kRows];
+#pragma unroll 1
+    for (int k = 0; k < 8 && base + k < most; k += kAhead) {
+      float4 o[kAhead][Q];
+      float wk[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const bool any = todo != 0;
-        const int src = any ? __ffs(todo) - 1 : 0;
-        todo &= todo - 1;
-        const int64_t first = __shfl_sync(0xffffffffu, row, src);
+      for (int c = 0; c < kAhead; ++c) {
+        wk[c] = __shfl_sync(0xffffffffu, w, group + k + c);
+        const float4* src =
+            reinterpret_cast<const float4*>(p.part_o + __shfl_sync(0xffffffffu, row, group + k + c) * D) + g;
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          const float x = __shfl_sync(0xffffffffu, w[r], src);
-          wk[k][r] = any ? x : 0.f;
-          if (wk[k][r] != 0.f) {
-            load_part<V>(o[k][r], p.part_o + (first + r) * D, lane);
-          } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) o[k][r][v] = 0.f;
-          }
-        }
+        for (int q = 0; q < Q; ++q) o[c][q] = wk[c] != 0.f ? __ldcs(src + 8 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
+      for (int c = 0; c < kAhead; ++c)
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
-#pragma unroll
-          for (int v = 0; v < V; ++v) acc[r][v] = fmaf(wk[k][r], o[k][r][v], acc[r][v]);
+        for (int q = 0; q < Q; ++q) {
+          acc[q].x = fmaf(wk[c], o[c][q].x, acc[q].x);
+          acc[q].y = fmaf(wk[c], o[c][q].y, acc[q].y);
+          acc[q].z = fmaf(wk[c], o[c][q].z, acc[q].z);
+          acc[q].w = fmaf(wk[c], o[c][q].w, acc[q].w);
+        }
     }
   }
+  if (!on) return;
+  const float inv = l > 0.f ? __frcp_rn(l) : 0.f;
+  uint2* dst = reinterpret_cast<uint2*>(p.out + (int64_t(tok) * p.H + head) * D) + g;
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    if (r >= nr) break;
-    const float inv = l[r] > 0.f ? 1.0f / l[r] : 0.f;
-    __nv_bfloat16* dst = p.out + (int64_t(tok[r]) * p.H + head[r]) * D;
-    if constexpr (V == 4) {
-      uint2 o;
-      o.x = pack_bf16x2(acc[r][0] * inv, acc[r][1] * inv);
-      o.y = pack_bf16x2(acc[r][2] * inv, acc[r][3] * inv);
-      reinterpret_cast<uint2*>(dst)[lane] = o;
-    } else {
-      reinterpret_cast<uint32_t*>(dst)[lane] = pack_bf16x2(acc[r][0] * inv, acc[r][1] * inv);
-    }
-    if (lane == 0 && p.lse)
-      p.lse[int64_t(head[r]) * p.max_tokens + tok[r]] = l[r] > 0.f ? m[r] + logf(l[r]) : -INFINITY;
-  }
+  for (int q = 0; q < Q; ++q)
+    dst[8 * q] = make_uint2(pack_bf16x2(acc[q].x * inv, acc[q].y * inv), pack_bf16x2(acc[q].z * inv, acc[q].w * inv));
+  if (g == 0 && p.lse) p.lse[int64_t(head) * p.max_tokens + tok] = l > 0.f ? m + logf(l) : -INFINITY;
 }
 
 constexpr int kCombineThreads = 256;
-constexpr int kCombineWarps = kCombineThreads / 32;
+constexpr int kCombineRows = kCombineThreads / 8;  // a block at a time
 
 // Launched while the attention still runs (programmatic dependent launch): what
 // does not depend on its results is read first.
@@ -1456,39 +1420,45 @@ template <int D>
 __global__ void __launch_bounds__(kCombineThreads, 3) batch_combine_kernel(const Params p) {
   const wf_batch_hdr* h = p.hdr;
   const Line line = line_of(p);
-  const bool nothing = h->fingerprint != p.fingerprint || line.total == 0;
-  const int warp = threadIdx.x >> 5;
-  const int np = h->prefix_units;
-  const int64_t rows = int64_t(h->ctoks) * p.H;  // at most 2^20 tokens x 2^12 heads
-  const int64_t first = int64_t(blockIdx.x) * kCombineWarps + warp, stride = int64_t(gridDim.x) * kCombineWarps;
-  const int ctas = h->ctas;
-  Parts none{};
+  if (h->fingerprint != p.fingerprint || line.total == 0) return;
+  const int np = h->prefix_units, ctas = h->ctas;
+  const int sub = threadIdx.x >> 3;
+  const Parts none{};
   bool waited = false;
-  // rows of one-tile units, a warp each
-  for (int64_t k = first; k < rows && !nothing; k += stride) {
-    const int32_t ct = int32_t(uint64_t(k) / uint32_t(p.H)), head = int32_t(k - int64_t(ct) * p.H);
-    const wf_batch_ctok at = p.ctok_list[ct];
-    const int32_t pu = at.tok / (2 * p.tile_tokens);
-    const wf_batch_unit u = p.units[at.unit], q = p.units[pu < np ? pu : at.unit];
-    const int64_t pre_u = p.pre[at.unit], pre_q = p.pre[pu < np ? pu : at.unit];
-    if (unit_direct(u, p.tile_tokens)) continue;  // a single tile, never cut
-    const int32_t kv = head / p.group, row_head = head - kv * p.group;
-    const int64_t s0 = int64_t(kv) * line.head_cost;
-    const Parts a = parts_of(p, line, u, s0 + pre_u, at.tok - u.tok0, row_head);
-    const Parts b = u.ptiles < 0 ? parts_of(p, line, q, s0 + pre_q, at.tok - q.tok0, row_head) : none;
+  // rows of one-tile units
+  const int64_t rows = int64_t(h->ctoks) * p.H;  // at most 2^20 tokens x 2^12 heads
+#pragma unroll 1
+  for (int64_t k0 = int64_t(blockIdx.x) * kCombineRows; k0 < rows; k0 += int64_t(gridDim.x) * kCombineRows) {
+    const uint32_t k = uint32_t(k0 + sub);  // (rows fit 32 bits)
+    const uint32_t ct = k / uint32_t(p.H);
+    const int32_t head = int32_t(k - ct * uint32_t(p.H)), kv = head / p.group, row_head = head - kv * p.group;
+    bool on = k < rows;
+    Parts a = none, b = none;
+    int32_t tok = 0;
+    if (on) {
+      const wf_batch_ctok at = p.ctok_list[ct];
+      tok = at.tok;
+      const int32_t pu = tok / (2 * p.tile_tokens), pi = pu < np ? pu : at.unit;
+      const wf_batch_unit u = p.units[at.unit], q = p.units[pi];
+      const int64_t s0 = int64_t(kv) * line.head_cost, su = s0 + p.pre[at.unit], sq = s0 + p.pre[pi];
+      on = !unit_direct(u, p.tile_tokens);  // a single tile, never cut
+      a = parts_of(p, line, u, su, tok - u.tok0, row_head);
+      if (u.ptiles < 0) b = parts_of(p, line, q, sq, tok - q.tok0, row_head);
+    }
     if (!waited) cudaGridDependencySynchronize();
     waited = true;
-    const int32_t toks[1] = {at.tok}, heads[1] = {head};
-    merge_rows<D, 1>(p, line, a, b, ct, head, 1, toks, heads);
+    merge_row<D>(p, line, on, a, b, int32_t(ct), head, tok);
   }
   if (!waited) cudaGridDependencySynchronize();
-  // rows of two-tile units that were cut, a warp for four rows of a tile; a unit is taken up at its first cut
-  if (p.max_tokens <= p.tile_tokens || nothing) return;
-  for (int k = int(first); k < ctas * 64; k += int(stride)) {
-    const int half = (k >> 5) & 1, row0 = (k & 31) * 4;
-    const Cut cut = p.cuts[k >> 6];
-    const int32_t live = (half ? cut.ntok - p.tile_tokens : p.tile_tokens) * p.group;
-    if (cut.n == 0 || row0 >= live) continue;
+  // rows of two-tile units that were cut; a unit is taken up at its first cut
+  if (p.max_tokens <= p.tile_tokens) return;
+  constexpr int kBlocks = 256 / kCombineRows;
+#pragma unroll 1
+  for (int k = blockIdx.x; k < ctas * kBlocks; k += gridDim.x) {
+    const int r = k % kBlocks * kCombineRows + sub, half = r >> 7, row = r & 127;
+    const Cut cut = p.cuts[k / kBlocks];
+    if (cut.n == 0) continue;
+    const bool on = row < (half ? cut.ntok - p.tile_tokens : p.tile_tokens) * p.group;
     Parts a;
     a.s = cut.s;
     a.shift = WF_BATCH_PAIR_SHIFT;
@@ -1497,15 +1467,10 @@ __global__ void __launch_bounds__(kCombineThreads, 3) batch_combine_kernel(const
     a.n = cut.n;
     a.pair = a.cut = a.own = true;
     a.half = half;
-    a.row = row0;
-    int32_t tok[4], head[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int32_t ti = (row0 + r) / p.group;
-      tok[r] = cut.tok0 + (half ? p.tile_tokens : 0) + ti;
-      head[r] = cut.head * p.group + (row0 + r - ti * p.group);
-    }
-    merge_rows<D, 4>(p, line, a, none, 0, 0, min(4, live - row0), tok, head);
+    a.row = row;
+    const int32_t ti = row / p.group;
+    merge_row<D>(p, line, on, a, none, 0, cut.head * p.group + (row - ti * p.group),
+                 cut.tok0 + (half ? p.tile_tokens : 0) + ti);
   }
 }
 
@@ -1579,9 +1544,9 @@ wf_status launch(const wf_batch_desc* d, const BatchLayout& L, const Params& p, 
     return WF_ERR_CUDA;
   batch_attn_kernel<D><<<L.ctas, kThreads, Cfg<D>::kSmemBytes, stream>>>(tq, tn, tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return WF_ERR_CUDA;
-  // a warp per merge_rows that can be needed, as long as they run at once
-  const int64_t warps = std::max(L.max_ctok * d->num_heads, d->max_tokens > L.tile_tokens ? int64_t(L.ctas) * 64 : 0);
-  const int64_t blocks = (warps + kCombineWarps - 1) / kCombineWarps, most = int64_t(L.ctas) * 8;
+  // as many blocks as the rows that may have to be merged fill, or as run at once a few times over
+  const int64_t rows = std::max(L.max_ctok * d->num_heads, d->max_tokens > L.tile_tokens ? int64_t(L.ctas) * 256 : 0);
+  const int64_t blocks = (rows + kCombineRows - 1) / kCombineRows, most = int64_t(L.ctas) * 16;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
