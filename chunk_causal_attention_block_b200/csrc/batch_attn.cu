@@ -1350,7 +1350,7 @@ template <int D>
 __device__ __forceinline__ void merge_row(const Params& p, const Line& line, bool on, const Parts& a, const Parts& b,
                                           int32_t ct, int32_t head, int32_t tok) {
   constexpr int Q = D / 32;  // float4s per lane: dims 4 (g + 8 q) .. + 3
-  constexpr int kAhead = 8 / Q;
+  constexpr int kAhead = 16 / Q;  // parts whose loads are in flight
   const int g = threadIdx.x & 7, group = threadIdx.x & 24;
   float m = -INFINITY, l = 0.f;
   float4 acc[Q];
@@ -1411,13 +1411,13 @@ __device__ __forceinline__ void merge_row(const Params& p, const Line& line, boo
   if (g == 0 && p.lse) p.lse[int64_t(head) * p.max_tokens + tok] = l > 0.f ? m + logf(l) : -INFINITY;
 }
 
-constexpr int kCombineThreads = 256;
+constexpr int kCombineThreads = 128;
 constexpr int kCombineRows = kCombineThreads / 8;  // a block at a time
 
 // Launched while the attention still runs (programmatic dependent launch): what
 // does not depend on its results is read first.
 template <int D>
-__global__ void __launch_bounds__(kCombineThreads, 3) batch_combine_kernel(const Params p) {
+__global__ void __launch_bounds__(kCombineThreads, 4) batch_combine_kernel(const Params p) {
   const wf_batch_hdr* h = p.hdr;
   const Line line = line_of(p);
   if (h->fingerprint != p.fingerprint || line.total == 0) return;
