@@ -115,6 +115,7 @@ extern "C" wf_status wf_batch_append(const wf_batch_desc* desc, const void* plan
   if (misaligned(plan) || misaligned(rope) || misaligned(q) || misaligned(k) || misaligned(v) || misaligned(q_rot) ||
       misaligned(k_pool) || misaligned(v_pool) || reinterpret_cast<uintptr_t>(slot_map) % 4)
     return WF_ERR_ALIGNMENT;
+  if (!wf::on_current_device(plan)) return WF_ERR_INVALID_ARG;
   AppendParams p{};
   p.hdr = static_cast<const wf_batch_hdr*>(plan);
   p.slot_map = slot_map;

@@ -8,8 +8,8 @@
 //
 // Work.  A unit is up to two 128-row tiles (tokens x group rows of one key
 // head, so a K/V tile is read once for a whole group) against a list of
-// 128-key tiles.  Rows of a request that fill half a tile or more run the
-// prefix's tiles and their own in one unit.  Rows of smaller requests are
+// 128-key tiles.  Rows of a request with more tokens than a row tile holds run
+// the prefix's tiles and their own in one unit.  Rows of smaller requests are
 // packed across requests for the prefix (each prefix key is then read once
 // for the whole batch) and run their own keys in units of their own.  The
 // units of all heads form one line of costs (the work list of
@@ -26,6 +26,19 @@
 // covers PV(m-2), so the softmax owns O when it sees S.  The online softmax
 // is the one of attn_sm100.cu (log2 domain, reference raised only when a
 // row's maximum grows by more than 2^8).
+//
+// Narrow items (at most 32 rows: a single token or a short proposal's own keys)
+// would leave three of a stream's four warps idle.  Their Q rows lie four
+// times in the Q tile, one copy for each warp; a warp takes 32 of the tile's
+// 128 keys, P goes to shared memory and the MMA forms O^T = V^T P^T, 32
+// columns wide.
+//
+// What bounds it.  Many single tokens: HBM (96 requests, up to 4000 own keys
+// each, 32760 shared, 12 heads: 250 us, 1.50 GB, 6.0 TB/s).  Long proposals:
+// the exponentials and MMAs of the two streams together, under the power limit
+// (2 x 4680 tokens over 42120 keys, 12 heads: 2.0-2.3 ms, 1.1-1.2 PFLOP/s of
+// visible pairs).  A few rows: latency (one token over 334 keys: 15 us, most
+// of it the host's).
 //
 // Warp roles (384 threads):
 //   warps 0-3, 4-7  softmax of stream 0 and 1
@@ -112,6 +125,12 @@ struct Params {
   int32_t cols, page_shift, block_tokens, max_tokens, max_ctok;
   int32_t stall_first_load;  // test hook: CTA 0 never issues its first K tile
 };
+
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+}
 
 constexpr int kXchBytes = 128 * 8;    // per stream: what its warps tell one another of narrow items' rows
 constexpr int kStageRows = 32 * 128;  // per softmax warp: 128 bytes of each of its rows, on their way out
@@ -1030,7 +1049,7 @@ __device__ __forceinline__ uint8_t* row_out(const Params& p, bool direct, int64_
                                             bool writes_lse, bool has_o) {
   if (row < 0) return nullptr;
   if (writes_lse) {
-    const float x = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+    const float x = l != 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;  // (a row's NaN stays one)
     if (!direct)
       p.part_lse[row] = x;
     else if (p.lse)
@@ -1053,7 +1072,7 @@ __device__ __forceinline__ void softmax_role(const Shared<D>& sh, const Params& 
   Pending pend;
   auto store_pending = [&](float sum) {
     uint8_t* dst = row_out<D>(p, pend.direct, pend.row, pend.lse, pend.m, sum, warp == 0, true);
-    store_columns<D>(o_tm + kNarrow * (ot ^ 1), dst, pend.direct, sum > 0.f ? __frcp_rn(sum) : 0.f, pend.rows);
+    store_columns<D>(o_tm + kNarrow * (ot ^ 1), dst, pend.direct, sum != 0.f ? __frcp_rn(sum) : 0.f, pend.rows);
     pend.on = false;
   };
   for (int it = 0;; ++it) {
@@ -1219,7 +1238,7 @@ __device__ __forceinline__ void softmax_role(const Shared<D>& sh, const Params& 
       tc_fence_after();
     }
     uint8_t* dst = row_out<D>(p, dest == kDirect, out_row, lse, m_ref, l, !narrow || warp == 0, !first);
-    if (!first && warp_live) store_rows<D>(sh, o_tm, dst, dest == kDirect, l > 0.f ? __frcp_rn(l) : 0.f);
+    if (!first && warp_live) store_rows<D>(sh, o_tm, dst, dest == kDirect, l != 0.f ? __frcp_rn(l) : 0.f);
   }
 }
 
@@ -1403,12 +1422,12 @@ __device__ __forceinline__ void merge_row(const Params& p, const Line& line, boo
     }
   }
   if (!on) return;
-  const float inv = l > 0.f ? __frcp_rn(l) : 0.f;
+  const float inv = l != 0.f ? __frcp_rn(l) : 0.f;
   uint2* dst = reinterpret_cast<uint2*>(p.out + (int64_t(tok) * p.H + head) * D) + g;
 #pragma unroll
   for (int q = 0; q < Q; ++q)
     dst[8 * q] = make_uint2(pack_bf16x2(acc[q].x * inv, acc[q].y * inv), pack_bf16x2(acc[q].z * inv, acc[q].w * inv));
-  if (g == 0 && p.lse) p.lse[int64_t(head) * p.max_tokens + tok] = l > 0.f ? m + logf(l) : -INFINITY;
+  if (g == 0 && p.lse) p.lse[int64_t(head) * p.max_tokens + tok] = l != 0.f ? m + logf(l) : -INFINITY;
 }
 
 constexpr int kCombineThreads = 128;
@@ -1420,7 +1439,10 @@ template <int D>
 __global__ void __launch_bounds__(kCombineThreads, 4) batch_combine_kernel(const Params p) {
   const wf_batch_hdr* h = p.hdr;
   const Line line = line_of(p);
-  if (h->fingerprint != p.fingerprint || line.total == 0) return;
+  if (h->fingerprint != p.fingerprint || line.total == 0) {
+    cudaGridDependencySynchronize();  // what follows on the stream waits for this kernel alone
+    return;
+  }
   const int np = h->prefix_units, ctas = h->ctas;
   const int sub = threadIdx.x >> 3;
   const Parts none{};
@@ -1584,12 +1606,14 @@ extern "C" wf_status wf_batch_attn(const wf_batch_desc* desc, const void* plan, 
   if (L.error != WF_OK) return L.error;
   if (!plan || !block_table || !q || !k_pool || !v_pool || !out || !workspace) return WF_ERR_INVALID_ARG;
   if (desc->max_prefix_pages > 0 && !prefix_table) return WF_ERR_INVALID_ARG;
+  if (out == q || out == k_pool || out == v_pool) return WF_ERR_INVALID_ARG;
   if (wf::misaligned(plan) || wf::misaligned(q) || wf::misaligned(k_pool) || wf::misaligned(v_pool) ||
       wf::misaligned(out) || wf::misaligned(workspace) || reinterpret_cast<uintptr_t>(lse) % 4 ||
       reinterpret_cast<uintptr_t>(block_table) % 4 || reinterpret_cast<uintptr_t>(prefix_table) % 4)
     return WF_ERR_ALIGNMENT;
   if (workspace_bytes < L.workspace_bytes) return WF_ERR_WORKSPACE;
   if (!(softmax_scale >= 0.f) || !std::isfinite(softmax_scale)) return WF_ERR_INVALID_ARG;
+  if (!wf::on_current_device(plan)) return WF_ERR_INVALID_ARG;
   const double scale = softmax_scale == 0.f ? 1.0 / std::sqrt(double(desc->head_dim)) : double(softmax_scale);
 
   wf::Params p{};

@@ -384,6 +384,16 @@ int sm_count() {
 
 namespace wf {
 
+bool on_current_device(const void* ptr) {
+  int dev = 0;
+  cudaPointerAttributes a;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaPointerGetAttributes(&a, ptr) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return (a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged) && a.device == dev;
+}
+
 BatchLayout batch_layout(const wf_batch_desc* d) {
   BatchLayout L{};
   L.error = WF_ERR_INVALID_ARG;
@@ -473,12 +483,16 @@ extern "C" wf_status wf_batch_tables(const wf_batch_desc* desc, const int32_t* c
   for (const void* i : in)
     for (const void* o : out)
       if (i && i == o) return WF_ERR_INVALID_ARG;
+  for (const void* const* o = out; o != out + 7; ++o)
+    for (const void* const* other = out; other != o; ++other)
+      if (*o && *o == *other) return WF_ERR_INVALID_ARG;
   for (const void* x : in)
     if (reinterpret_cast<uintptr_t>(x) % 4) return WF_ERR_ALIGNMENT;
   for (const void* x : out)
     if (reinterpret_cast<uintptr_t>(x) % 4) return WF_ERR_ALIGNMENT;
   if (reinterpret_cast<uintptr_t>(plan) % 16) return WF_ERR_ALIGNMENT;
   if (plan_bytes < L.plan_bytes) return WF_ERR_WORKSPACE;
+  if (!wf::on_current_device(plan)) return WF_ERR_INVALID_ARG;
 
   TablesParams p{};
   p.cached = cached;
@@ -516,10 +530,11 @@ extern "C" wf_status wf_batch_tables(const wf_batch_desc* desc, const int32_t* c
   p.fingerprint = L.fingerprint;
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  // Small blocks where a thread or two per request and the tokens do with
-  // them: 5 requests take 5.6 us with 256 threads a block, 7.2 us with 1024;
-  // 1024 requests 8.9 us with 1024, 10.3 us with 256.
-  return p.B <= 512 ? launch_tables<256>(p, st) : launch_tables<1024>(p, st);
+  // Blocks of 256 or 1024 threads.  A small block starts and scans sooner, a
+  // large one has a thread for every request: 5 requests 4.9 us with 256 and
+  // 5.8 us with 1024, 64 requests 5.0 and 6.2 us; 256 requests 7.2 and 7.0 us,
+  // 512 9.8 and 8.2 us, 1024 14.4 and 12.0 us, 8192 119 and 58 us.
+  return p.B <= 128 ? launch_tables<256>(p, st) : launch_tables<1024>(p, st);
 }
 
 extern "C" wf_status wf_batch_status(const void* plan, wf_stream_t stream, int32_t* detail) {

@@ -13,7 +13,9 @@
 // Key tiles are shared out to CTAs by cost.  A tile against two row tiles
 // (256 rows) costs 1 << WF_BATCH_PAIR_SHIFT, against one 1 <<
 // WF_BATCH_SINGLE_SHIFT, and every unit WF_BATCH_UNIT_COST more for filling
-// and draining the pipeline.
+// and draining the pipeline.  (A single tile at the cost of a pair: 64 decoding
+// requests 54 -> 67 us, a round of two branches 2.1 -> 2.6 ms.  A unit at 1, 2,
+// 3 or 8 instead of 4: within 6% both ways, as the cuts happen to fall.)
 #define WF_BATCH_PAIR_SHIFT 3
 #define WF_BATCH_SINGLE_SHIFT 2
 #define WF_BATCH_UNIT_COST 4
@@ -77,5 +79,8 @@ struct BatchLayout {
 };
 
 BatchLayout batch_layout(const wf_batch_desc* d);
+
+// Whether ptr is memory of the current device: elsewhere a kernel would fault on it.
+bool on_current_device(const void* ptr);
 
 }  // namespace wf

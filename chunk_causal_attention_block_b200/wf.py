@@ -267,30 +267,40 @@ def wf_batch_workspace_bytes(desc: BatchDesc) -> int:
     return lib().wf_batch_workspace_bytes(ctypes.byref(desc))
 
 
-def _room(where, x, n, size):
-    """Address of x, which must be dense and hold n elements of `size` bytes.  Raw addresses and None pass as they are:
-    their owner vouches for them."""
+def _room(where, dev, x, n, size):
+    """Address of x, which must be dense, hold n elements of `size` bytes and lie on device `dev` (that of the call's
+    plan).  Raw addresses and None pass as they are: their owner vouches for them."""
     try:
-        if x.is_contiguous() and x.itemsize == size and x.numel() >= n:
+        if x.is_contiguous() and x.itemsize == size and x.numel() >= n and (x.get_device() == dev or dev is None):
             return x.data_ptr()
     except AttributeError:
         return _ptr(x)
-    raise WfError(WF_ERR_INVALID_ARG, f"{where}: {x.numel()} elements of {x.itemsize} bytes (dense: "
-                                      f"{x.is_contiguous()}) where {n} of {size} are needed")
+    raise WfError(WF_ERR_INVALID_ARG, f"{where}: {x.numel()} elements of {x.itemsize} bytes on {x.device} (dense: "
+                                      f"{x.is_contiguous()}) where {n} of {size} are needed on the plan's device")
+
+
+def _device(plan):
+    """Device of a tensor; None for a raw address.  A host tensor's is -1, which no tensor of a call may have."""
+    try:
+        dev = plan.get_device()
+    except AttributeError:
+        return None
+    return dev if dev >= 0 else -2
 
 
 def wf_batch_tables(desc: BatchDesc, cached, fresh, prefix_len, free_pages, free_head, free_head_out, block_table,
                     token_start, slot_map, positions, plan, held=None, held_out=None, stream=None, num_free=None,
                     plan_bytes=None):
-    w, B, T = "wf_batch_tables", desc.max_requests, desc.max_tokens
+    w, d, B, T = "wf_batch_tables", _device(plan), desc.max_requests, desc.max_tokens
     nf = num_free if num_free is not None else free_pages.numel()
     pb = plan_bytes if plan_bytes is not None else _nbytes(plan)
+    h = None if held is None else _room(w, d, held, B, 4)
+    ho = None if held_out is None else _room(w, d, held_out, B, 4)
     _check(lib().wf_batch_tables(
-        ctypes.byref(desc), _room(w, cached, B, 4), _room(w, fresh, B, 4), _room(w, prefix_len, 1, 4),
-        _room(w, held, B, 4), _room(w, free_pages, nf, 4), nf, _room(w, free_head, 1, 4),
-        _room(w, free_head_out, 1, 4), _room(w, held_out, B, 4), _room(w, block_table, B * desc.max_request_pages, 4),
-        _room(w, token_start, B + 1, 4), _room(w, slot_map, T, 4), _room(w, positions, T, 4), _ptr(plan), pb,
-        _stream(stream)), w)
+        ctypes.byref(desc), _room(w, d, cached, B, 4), _room(w, d, fresh, B, 4), _room(w, d, prefix_len, 1, 4), h,
+        _room(w, d, free_pages, nf, 4), nf, _room(w, d, free_head, 1, 4), _room(w, d, free_head_out, 1, 4), ho,
+        _room(w, d, block_table, B * desc.max_request_pages, 4), _room(w, d, token_start, B + 1, 4),
+        _room(w, d, slot_map, T, 4), _room(w, d, positions, T, 4), _ptr(plan), pb, _stream(stream)), w)
 
 
 def wf_batch_status(plan, stream=None):
@@ -300,24 +310,24 @@ def wf_batch_status(plan, stream=None):
 
 def wf_batch_append(desc: BatchDesc, plan, slot_map, k, v, k_pool, v_pool, q=None, rope=None, q_rot=None, stream=None):
     # the step may hold fewer tokens than max_tokens: only the device knows, so room for all is asked for
-    w, T, kv_row = "wf_batch_append", desc.max_tokens, desc.num_kv_heads * desc.head_dim
+    w, d, T, kv_row = "wf_batch_append", _device(plan), desc.max_tokens, desc.num_kv_heads * desc.head_dim
     pool, q_size = desc.pool_pages * desc.page_tokens * kv_row, T * desc.num_heads * desc.head_dim
     _check(lib().wf_batch_append(
-        ctypes.byref(desc), _ptr(plan), _room(w, slot_map, T, 4), _room(w, rope, T * desc.head_dim, 4),
-        _room(w, q, q_size, 2), _room(w, k, T * kv_row, 2), _room(w, v, T * kv_row, 2), _room(w, q_rot, q_size, 2),
-        _room(w, k_pool, pool, 2), _room(w, v_pool, pool, 2), _stream(stream)), w)
+        ctypes.byref(desc), _ptr(plan), _room(w, d, slot_map, T, 4), _room(w, d, rope, T * desc.head_dim, 4),
+        _room(w, d, q, q_size, 2), _room(w, d, k, T * kv_row, 2), _room(w, d, v, T * kv_row, 2),
+        _room(w, d, q_rot, q_size, 2), _room(w, d, k_pool, pool, 2), _room(w, d, v_pool, pool, 2), _stream(stream)), w)
 
 
 def wf_batch_attn(desc: BatchDesc, plan, block_table, prefix_table, q, k_pool, v_pool, out, lse=None,
                   softmax_scale=0.0, workspace=None, stream=None, workspace_bytes=None):
-    w, T, H = "wf_batch_attn", desc.max_tokens, desc.num_heads
+    w, d, T, H = "wf_batch_attn", _device(plan), desc.max_tokens, desc.num_heads
     q_size, pool = T * H * desc.head_dim, desc.pool_pages * desc.page_tokens * desc.num_kv_heads * desc.head_dim
     wb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
     _check(lib().wf_batch_attn(
-        ctypes.byref(desc), _ptr(plan), _room(w, block_table, desc.max_requests * desc.max_request_pages, 4),
-        _room(w, prefix_table, desc.max_prefix_pages, 4), _room(w, q, q_size, 2), _room(w, k_pool, pool, 2),
-        _room(w, v_pool, pool, 2), _room(w, out, q_size, 2), _room(w, lse, T * H, 4), softmax_scale, _ptr(workspace),
-        wb, _stream(stream)), w)
+        ctypes.byref(desc), _ptr(plan), _room(w, d, block_table, desc.max_requests * desc.max_request_pages, 4),
+        _room(w, d, prefix_table, desc.max_prefix_pages, 4), _room(w, d, q, q_size, 2), _room(w, d, k_pool, pool, 2),
+        _room(w, d, v_pool, pool, 2), _room(w, d, out, q_size, 2), _room(w, d, lse, T * H, 4), softmax_scale,
+        _room(w, d, workspace, 0, 1), wb, _stream(stream)), w)
 
 
 def wf_synth_fill(dst, dtype, seed, tensor, tag, n_first, nchunks, C, H, D, kscale=False, stream=None):

@@ -166,3 +166,34 @@ def test_oracle_attention_by_hand():
 
 def test_struct_sizes_match_the_header():
     assert ctypes.sizeof(wf.BatchDesc) == 48
+
+
+@pytest.mark.parametrize("name", ["q", "k_pool", "v_pool"])
+def test_attention_does_not_write_over_what_it_reads(name):
+    # other thread blocks may still read the rows that one of them stores
+    with pytest.raises(wf.WfError) as e:
+        attn_with(**{name: 7 << 20})
+    assert e.value.code == wf.WF_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("a,b", [("slot_map", "positions"), ("token_start", "slot_map"), ("plan", "block_table"),
+                                 ("free_head_out", "token_start")])
+def test_tables_need_a_buffer_for_each_result(a, b):
+    with pytest.raises(wf.WfError) as e:
+        tables_with(**{a: ARGS[b] << 20})
+    assert e.value.code == wf.WF_ERR_INVALID_ARG
+
+
+def test_memory_that_is_not_the_devices_is_refused():
+    # every argument is well formed, but the plan is no memory of the current device (here: of none at all)
+    d = desc()
+    for call in (tables_with, append_with, attn_with):
+        with pytest.raises(wf.WfError) as e:
+            call()
+        assert e.value.code == wf.WF_ERR_INVALID_ARG
+    torch = pytest.importorskip("torch")
+    host = torch.zeros(wf.wf_batch_plan_bytes(d), dtype=torch.uint8)
+    x = torch.zeros(64, 8, 128, dtype=torch.bfloat16)
+    with pytest.raises(wf.WfError) as e:
+        wf.wf_batch_append(d, host, torch.zeros(64, dtype=torch.int32), x, x, x, x)
+    assert e.value.code == wf.WF_ERR_INVALID_ARG

@@ -330,3 +330,36 @@ def test_pages_outside_the_pool_are_not_touched():
     assert (slots == -1).any()
     assert wf.wf_attn_workspace_status(s.ws, s.stream)[0] == wf.WF_OK
     assert not torch.isnan(s.out[:s.T].float()).any()
+
+
+def test_host_memory_is_refused():
+    s = Step([20, 3], [2, 30], prefix=50).run()
+    for name in ("cached", "block_table", "positions"):
+        with pytest.raises(wf.WfError) as e:
+            s.tables(**{name: s.d[name].cpu()})
+        assert e.value.code == wf.WF_ERR_INVALID_ARG
+    with pytest.raises(wf.WfError) as e:
+        s.tables(plan=s.d["plan"].cpu().pin_memory().data_ptr(), plan_bytes=s.d["plan"].numel())
+    assert e.value.code == wf.WF_ERR_INVALID_ARG
+    with pytest.raises(wf.WfError) as e:
+        wf.wf_batch_attn(s.desc, s.d["plan"], s.d["block_table"], s.prefix_dev, s.q_rot.cpu(), s.k_pool, s.v_pool, s.out,
+                         s.lse, workspace=s.ws, stream=s.stream)
+    assert e.value.code == wf.WF_ERR_INVALID_ARG
+    s.check_attention()  # nothing of it ran
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_row_of_nans_stays_one_and_alone(D):
+    # rows of every kind of unit: narrow, shared, whole tiles, merged parts
+    s = Step([200, 3, 900, 0], [1, 9, 1, 300], prefix=500, H=4, Hkv=2, D=D, num_ctas=23)
+    s.run()
+    s.check_attention()
+    out, lse = s.out.clone(), s.lse.clone()
+    bad = torch.zeros(s.q_rot.shape[:2], dtype=torch.bool, device="cuda")
+    for t, h in ((0, 1), (4, 0), (10, 3), (11, 2), (150, 0), (310, 1)):
+        bad[t, h] = True
+        s.q_rot[t, h, 5] = float("nan")
+    s.attend()
+    assert wf.wf_attn_workspace_status(s.ws, s.stream)[0] == wf.WF_OK
+    assert torch.isnan(s.out[bad].float()).all() and torch.isnan(s.lse.T[bad]).all()
+    assert torch.equal(s.out[~bad], out[~bad]) and torch.equal(s.lse.T[~bad], lse.T[~bad])
