@@ -1084,8 +1084,11 @@ __device__ __forceinline__ void softmax_role(const Shared<D>& sh, const Params& 
     const bool narrow = item_field(item, offsetof(Item, head)) & 1;
     if (pend.on && !narrow) {
       // nothing to overlap it with (the end), or an item that uses all of O
+      // (between tiles, S(m) separates one exchange from the next; here the stream meets before and after)
       float none, sum;
+      if (!stream_sync<D>(sh, p, t, x_phase)) return;
       if (!exchange<D>(sh, p, t, 0.f, pend.l, none, sum, x_phase)) return;
+      if (!stream_sync<D>(sh, p, t, x_phase)) return;
       if (!warp_wait(sh, p, C::kOFull + t, o_phase, 24 + t)) return;
       o_phase ^= 1;
       tc_fence_after();
