@@ -407,6 +407,25 @@ __device__ __forceinline__ void scheduler(const Shared<D>& sh, const Params& p, 
     const int32_t w = tile_shift(r.ntok, p.tile_tokens);
     if (have) share_tiles(s, w, r.ktiles, x.lo, x.hi, j0, j1);
     more = __all_sync(0xffffffffu, !have || s < x.hi);
+    if (start && lane == 0) {
+      // for the merging: whether the share begins with the first cut of a two-tile unit (written before any
+      // wait can give up: the merging kernel reads it all the same)
+      const Line line = line_of(p);
+      Cut k{};
+      if (j0 > 0 && j0 < j1 && r.req >= 0 && r.ntok > p.tile_tokens) {
+        k.c0 = share_of(line, s);
+        if (share_of(line, s + (int64_t(j0 - 1) << w)) == k.c0) {
+          k.s = s;
+          k.head = head;
+          k.tok0 = r.tok0;
+          k.ntok = r.ntok;
+          k.ktiles = r.ktiles;
+          k.n = share_of(line, s + (int64_t(r.ktiles - 1) << w)) - k.c0 + 1;
+        }
+      }
+      p.cuts[blockIdx.x] = k;
+    }
+    start = false;
     uint32_t todo = __ballot_sync(0xffffffffu, j0 < j1);
     while (todo) {
       const int src = __ffs(todo) - 1;
@@ -450,24 +469,6 @@ __device__ __forceinline__ void scheduler(const Shared<D>& sh, const Params& p, 
       tile0 += n;
       ++it;
     }
-    if (start && lane == 0) {
-      // for the merging: whether the share begins with the first cut of a two-tile unit
-      const Line line = line_of(p);
-      Cut k{};
-      if (j0 > 0 && j0 < j1 && r.req >= 0 && r.ntok > p.tile_tokens) {
-        k.c0 = share_of(line, s);
-        if (share_of(line, s + (int64_t(j0 - 1) << w)) == k.c0) {
-          k.s = s;
-          k.head = head;
-          k.tok0 = r.tok0;
-          k.ntok = r.ntok;
-          k.ktiles = r.ktiles;
-          k.n = share_of(line, s + (int64_t(r.ktiles - 1) << w)) - k.c0 + 1;
-        }
-      }
-      p.cuts[blockIdx.x] = k;
-    }
-    start = false;
     u += 32;
     if (u >= x.units) {
       // the next head's first unit starts where this head ends

@@ -363,3 +363,20 @@ def test_a_row_of_nans_stays_one_and_alone(D):
     assert wf.wf_attn_workspace_status(s.ws, s.stream)[0] == wf.WF_OK
     assert torch.isnan(s.out[bad].float()).all() and torch.isnan(s.lse.T[bad]).all()
     assert torch.equal(s.out[~bad], out[~bad]) and torch.equal(s.lse.T[~bad], lse.T[~bad])
+
+
+def test_an_expired_wait_in_a_fresh_workspace_leaves_other_rows_alone(monkeypatch):
+    # whatever the workspace held behind its first 256 bytes, nothing outside the step's rows is written
+    for kw in (dict(cached=[0, 7], fresh=[900, 300], num_ctas=23), dict(cached=[300, 20], fresh=[1, 40], prefix=700)):
+        s = Step(**kw, spare_tokens=400)
+        s.tables()
+        s.append()
+        s.ws[256:] = 1
+        monkeypatch.setenv("WF_WAIT_TIMEOUT_MS", "100")
+        monkeypatch.setenv("WF_DEBUG_STALL_FIRST_LOAD", "1")
+        s.attend()
+        code, _ = wf.wf_attn_workspace_status(s.ws, s.stream)
+        monkeypatch.delenv("WF_DEBUG_STALL_FIRST_LOAD")
+        monkeypatch.delenv("WF_WAIT_TIMEOUT_MS")
+        assert code == wf.WF_ERR_DEVICE_TIMEOUT
+        assert (s.out[s.T:] == SENTINEL).all() and (s.lse[:, s.T:] == SENTINEL).all()
