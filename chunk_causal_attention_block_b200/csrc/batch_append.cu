@@ -111,7 +111,12 @@ extern "C" wf_status wf_batch_append(const wf_batch_desc* desc, const void* plan
   if (L.error != WF_OK) return L.error;
   if (!plan || !slot_map || !k || !v || !k_pool || !v_pool) return WF_ERR_INVALID_ARG;
   if (rope ? (!q || !q_rot) : (q || q_rot)) return WF_ERR_INVALID_ARG;  // Q only turns: without angles there is nothing to do
-  if (k == k_pool || v == v_pool || k_pool == v_pool) return WF_ERR_INVALID_ARG;
+  // nothing that other threads still read is written over (a Q row is turned by the threads that read it)
+  const void* in[] = {k, v, rope, slot_map, plan};
+  for (const void* i : in)
+    if (i && (i == k_pool || i == v_pool || i == q_rot)) return WF_ERR_INVALID_ARG;
+  if (k_pool == v_pool || (q && (q == k_pool || q == v_pool || q_rot == k_pool || q_rot == v_pool)))
+    return WF_ERR_INVALID_ARG;
   if (misaligned(plan) || misaligned(rope) || misaligned(q) || misaligned(k) || misaligned(v) || misaligned(q_rot) ||
       misaligned(k_pool) || misaligned(v_pool) || reinterpret_cast<uintptr_t>(slot_map) % 4)
     return WF_ERR_ALIGNMENT;

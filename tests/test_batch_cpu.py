@@ -197,3 +197,12 @@ def test_memory_that_is_not_the_devices_is_refused():
     with pytest.raises(wf.WfError) as e:
         wf.wf_batch_append(d, host, torch.zeros(64, dtype=torch.int32), x, x, x, x)
     assert e.value.code == wf.WF_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("a,b", [("q_rot", "k"), ("q_rot", "v"), ("q_rot", "rope"), ("q_rot", "k_pool"), ("v_pool", "k"),
+                                 ("k_pool", "q"), ("k_pool", "rope")])
+def test_append_does_not_write_over_what_it_reads(a, b):
+    at = dict(k=3 << 20, v=4 << 20, k_pool=5 << 20, q=7 << 20, rope=8 << 20)
+    with pytest.raises(wf.WfError) as e:
+        append_with(**{a: at[b]})
+    assert e.value.code == wf.WF_ERR_INVALID_ARG
