@@ -1,4 +1,5 @@
-"""Build libwf.so in-tree with nvcc for sm_100a.
+"""Build libwf.so in-tree with nvcc for sm_100a, and _wf_torch.so, which checks
+torch tensors for the batch calls, with the host compiler.
 
     python -m chunk_causal_attention_block_b200.build [--verbose]
 
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libwf.so")
+TORCH_SRC = os.path.join(CSRC, "wf_torch.cc")
+TORCH_LIB = os.path.join(PKG, "_wf_torch.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
@@ -63,7 +67,27 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
+    _build_torch_calls(verbose)
     return LIB
+
+
+def _build_torch_calls(verbose: bool):
+    newest = max(os.path.getmtime(f) for f in (TORCH_SRC, os.path.join(INCLUDE, "wf.h")))
+    if os.path.exists(TORCH_LIB) and os.path.getmtime(TORCH_LIB) >= newest:
+        return
+    import torch
+    # (the g++ on the path, whose C++ runtime torch shares; one that links the runtime statically cannot catch
+    # torch's exceptions)
+    root = os.path.dirname(torch.__file__)
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-o", TORCH_LIB, TORCH_SRC,
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
 
 
 if __name__ == "__main__":

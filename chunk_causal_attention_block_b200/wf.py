@@ -4,6 +4,8 @@ Argument marshalling only: every step of the hot path runs in the library's
 CUDA kernels.  Functions keep the C names.  Tensors may be passed as torch
 tensors (their data_ptr is used) or raw integer addresses; streams as
 ``torch.cuda.Stream`` or integer handles (``None`` = legacy default stream).
+The batch calls check their tensors (device, element size, layout, room) in
+``_wf_torch.so`` before they pass them on; the others take any address.
 Loading fails loudly when the library has not been built: there is no
 fallback implementation.
 """
@@ -267,40 +269,37 @@ def wf_batch_workspace_bytes(desc: BatchDesc) -> int:
     return lib().wf_batch_workspace_bytes(ctypes.byref(desc))
 
 
-def _room(where, dev, x, n, size):
-    """Address of x, which must be dense, hold n elements of `size` bytes and lie on device `dev` (that of the call's
-    plan).  Raw addresses and None pass as they are: their owner vouches for them."""
-    try:
-        if x.is_contiguous() and x.itemsize == size and x.numel() >= n and (x.get_device() == dev or dev is None):
-            return x.data_ptr()
-    except AttributeError:
-        return _ptr(x)
-    raise WfError(WF_ERR_INVALID_ARG, f"{where}: {x.numel()} elements of {x.itemsize} bytes on {x.device} (dense: "
-                                      f"{x.is_contiguous()}) where {n} of {size} are needed on the plan's device")
+_torch_calls = None
 
 
-def _device(plan):
-    """Device of a tensor; None for a raw address.  A host tensor's is -1, which no tensor of a call may have."""
-    try:
-        dev = plan.get_device()
-    except AttributeError:
-        return None
-    return dev if dev >= 0 else -2
+def _batch_calls():
+    """The batch calls' native argument checks (csrc/wf_torch.cc), bound to the loaded library."""
+    global _torch_calls
+    if _torch_calls is None:
+        import torch  # noqa: F401  (its libraries have to be loaded first)
+        try:
+            from . import _wf_torch as m
+        except ImportError as e:
+            raise RuntimeError("_wf_torch.so is not built (or for another torch); run "
+                               "`python -m chunk_causal_attention_block_b200.build`") from e
+        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                 for f in (lib().wf_batch_tables, lib().wf_batch_append, lib().wf_batch_attn)))
+        _torch_calls = m
+    return _torch_calls
+
+
+def _check_batch(code, where: str):
+    if code != WF_OK:
+        # a reason in words: the arguments did not get as far as the library
+        raise WfError(code, where) if isinstance(code, int) else WfError(WF_ERR_INVALID_ARG, f"{where}: {code}")
 
 
 def wf_batch_tables(desc: BatchDesc, cached, fresh, prefix_len, free_pages, free_head, free_head_out, block_table,
                     token_start, slot_map, positions, plan, held=None, held_out=None, stream=None, num_free=None,
                     plan_bytes=None):
-    w, d, B, T = "wf_batch_tables", _device(plan), desc.max_requests, desc.max_tokens
-    nf = num_free if num_free is not None else free_pages.numel()
-    pb = plan_bytes if plan_bytes is not None else _nbytes(plan)
-    h = None if held is None else _room(w, d, held, B, 4)
-    ho = None if held_out is None else _room(w, d, held_out, B, 4)
-    _check(lib().wf_batch_tables(
-        ctypes.byref(desc), _room(w, d, cached, B, 4), _room(w, d, fresh, B, 4), _room(w, d, prefix_len, 1, 4), h,
-        _room(w, d, free_pages, nf, 4), nf, _room(w, d, free_head, 1, 4), _room(w, d, free_head_out, 1, 4), ho,
-        _room(w, d, block_table, B * desc.max_request_pages, 4), _room(w, d, token_start, B + 1, 4),
-        _room(w, d, slot_map, T, 4), _room(w, d, positions, T, 4), _ptr(plan), pb, _stream(stream)), w)
+    _check_batch(_batch_calls().tables(desc, plan, cached, fresh, prefix_len, held, free_pages, num_free, free_head,
+                                       free_head_out, held_out, block_table, token_start, slot_map, positions, plan_bytes,
+                                       _stream(stream)), "wf_batch_tables")
 
 
 def wf_batch_status(plan, stream=None):
@@ -309,25 +308,14 @@ def wf_batch_status(plan, stream=None):
 
 
 def wf_batch_append(desc: BatchDesc, plan, slot_map, k, v, k_pool, v_pool, q=None, rope=None, q_rot=None, stream=None):
-    # the step may hold fewer tokens than max_tokens: only the device knows, so room for all is asked for
-    w, d, T, kv_row = "wf_batch_append", _device(plan), desc.max_tokens, desc.num_kv_heads * desc.head_dim
-    pool, q_size = desc.pool_pages * desc.page_tokens * kv_row, T * desc.num_heads * desc.head_dim
-    _check(lib().wf_batch_append(
-        ctypes.byref(desc), _ptr(plan), _room(w, d, slot_map, T, 4), _room(w, d, rope, T * desc.head_dim, 4),
-        _room(w, d, q, q_size, 2), _room(w, d, k, T * kv_row, 2), _room(w, d, v, T * kv_row, 2),
-        _room(w, d, q_rot, q_size, 2), _room(w, d, k_pool, pool, 2), _room(w, d, v_pool, pool, 2), _stream(stream)), w)
+    _check_batch(_batch_calls().append(desc, plan, slot_map, rope, q, k, v, q_rot, k_pool, v_pool, _stream(stream)),
+                 "wf_batch_append")
 
 
 def wf_batch_attn(desc: BatchDesc, plan, block_table, prefix_table, q, k_pool, v_pool, out, lse=None,
                   softmax_scale=0.0, workspace=None, stream=None, workspace_bytes=None):
-    w, d, T, H = "wf_batch_attn", _device(plan), desc.max_tokens, desc.num_heads
-    q_size, pool = T * H * desc.head_dim, desc.pool_pages * desc.page_tokens * desc.num_kv_heads * desc.head_dim
-    wb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
-    _check(lib().wf_batch_attn(
-        ctypes.byref(desc), _ptr(plan), _room(w, d, block_table, desc.max_requests * desc.max_request_pages, 4),
-        _room(w, d, prefix_table, desc.max_prefix_pages, 4), _room(w, d, q, q_size, 2), _room(w, d, k_pool, pool, 2),
-        _room(w, d, v_pool, pool, 2), _room(w, d, out, q_size, 2), _room(w, d, lse, T * H, 4), softmax_scale,
-        _room(w, d, workspace, 0, 1), wb, _stream(stream)), w)
+    _check_batch(_batch_calls().attn(desc, plan, block_table, prefix_table, q, k_pool, v_pool, out, lse, softmax_scale,
+                                     workspace, workspace_bytes, _stream(stream)), "wf_batch_attn")
 
 
 def wf_synth_fill(dst, dtype, seed, tensor, tag, n_first, nchunks, C, H, D, kscale=False, stream=None):

@@ -206,3 +206,21 @@ def test_append_does_not_write_over_what_it_reads(a, b):
     with pytest.raises(wf.WfError) as e:
         append_with(**{a: at[b]})
     assert e.value.code == wf.WF_ERR_INVALID_ARG
+
+
+def test_arguments_of_other_types_are_refused():
+    torch = pytest.importorskip("torch")
+    d = desc()
+    at = 1 << 20
+    for call in (lambda: tables_with(cached=np.zeros(4, np.int32)), lambda: tables_with(num_free="5"),
+                 lambda: tables_with(num_free=None), lambda: tables_with(num_free=2 ** 40), lambda: tables_with(fresh=2.0),
+                 lambda: append_with(k=[1, 2]), lambda: attn_with(softmax_scale="1"), lambda: attn_with(workspace_bytes=None),
+                 lambda: attn_with(q=2 ** 70), lambda: attn_with(lse=torch.zeros(10 ** 4)),
+                 lambda: attn_with(q=torch.zeros(64, 8, 128, dtype=torch.bfloat16).to_sparse())):
+        with pytest.raises(wf.WfError) as e:
+            call()
+        assert e.value.code == wf.WF_ERR_INVALID_ARG
+    for other in (wf.RoundDesc(), b"12", None):
+        with pytest.raises(TypeError):
+            wf.wf_batch_append(other, at, at, at, at, 2 * at, 3 * at)
+    assert bytes(d) == bytes(desc())
