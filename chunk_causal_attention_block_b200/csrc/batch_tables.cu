@@ -99,7 +99,7 @@ __device__ void block_scan(int64_t (&v)[N], int64_t (&total)[N], int64_t* scratc
 struct Sums {
   int64_t w[3];
   __device__ __forceinline__ void add(int32_t f, int32_t new_pages, int32_t tile_tokens) {
-    const int32_t tiles = (f + tile_tokens - 1) / tile_tokens;
+    const int32_t tiles = f <= tile_tokens ? f > 0 : (f + tile_tokens - 1) / tile_tokens;  // (a division takes 30 instructions)
     w[0] += f;
     w[1] += (int64_t(new_pages) << 24) + ((tiles & 1) ? f - (tiles - 1) * tile_tokens : 0);
     w[2] += (int64_t((tiles + 1) / 2) << 16) + (f > 0 && f <= tile_tokens);
@@ -125,6 +125,19 @@ __device__ __forceinline__ int last_not_above(const int32_t* a, int n, int32_t x
 }
 
 __device__ __forceinline__ int32_t ceil_shift(int64_t x, int s) { return int32_t((x + (int64_t(1) << s) - 1) >> s); }
+
+__device__ __forceinline__ int64_t unit_cost(const TablesParams& p, int32_t ntok, int32_t ktiles) {
+  const int shift = ntok > p.tile_tokens ? WF_BATCH_PAIR_SHIFT : WF_BATCH_SINGLE_SHIFT;
+  return ktiles > 0 ? (int64_t(ktiles) << shift) + WF_BATCH_UNIT_COST : 0;
+}
+
+// Returns the unit's cost.  (Stored field by field, 1024 units took 8000 cycles.)
+__device__ __forceinline__ int64_t store_unit(const TablesParams& p, int u, const wf_batch_unit& r) {
+  int4* dst = reinterpret_cast<int4*>(p.units + u);
+  dst[0] = make_int4(r.req, r.tok0, r.ntok, r.ktiles);
+  dst[1] = make_int4(r.ptiles, r.cbase, r.pos0, r.len);
+  return unit_cost(p, r.ntok, r.ktiles);
+}
 
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesParams p) {
@@ -185,6 +198,7 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesPara
   // (With half a tile as the limit, 48 requests of 1 to 20 tokens, 5 heads to a
   // key head, took 133 us on a prefix of 4680: the larger ones read it alone.)
   const bool shared = prefix > 0 && sum_small(total) >= 2;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     const int32_t c = __ldg(p.cached + b), f = __ldg(p.fresh + b);
     const int32_t h = p.held ? __ldg(p.held + b) : ceil_shift(c, p.page_shift);
@@ -238,68 +252,72 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesPara
     return;
   }
 
-  // ---- block 0: the attention's units and the running sum of their costs
+  // ---- block 0: the attention's units (prefix units, then own ones) and the
+  // running sum of their costs.  A thread makes consecutive units of each kind,
+  // so that one scan does whatever their number, and keeps the first's cost.
   const int32_t ptiles = (prefix + 127) >> 7;
-  const int32_t own = s_unit[p.B];
-  for (int u = tid; u < np; u += kThreads) {
-    wf_batch_unit r;
-    r.req = -1;
-    r.tok0 = u * pair_tokens;
-    r.ntok = min(pair_tokens, tokens - r.tok0);
-    r.ktiles = 0;
-    r.ptiles = ptiles;
-    r.cbase = -1;
-    r.pos0 = 0;
-    r.len = 0;
-    p.units[u] = r;
+  const int32_t units = np + s_unit[p.B];
+  int32_t first[2], behind[2];  // units of each kind that this thread makes
+#pragma unroll
+  for (int kind = 0; kind < 2; ++kind) {
+    const int32_t begin = kind ? np : 0, end = kind ? units : np;
+    const int32_t n = (end - begin + kThreads - 1) / kThreads;
+    first[kind] = min(begin + tid * n, end);
+    behind[kind] = min(first[kind] + n, end);
   }
-  for (int u = tid; u < own; u += kThreads) {
-    const int b = last_not_above(s_unit, p.B, u);
-    const int32_t c = p.cached[b], f = s_start[b + 1] - s_start[b], i0 = (u - s_unit[b]) * pair_tokens;
+  int64_t sum[2] = {0, 0}, all_costs[2], cost0[2] = {0, 0};
+  for (int u = first[0]; u < behind[0]; ++u) {
+    const int32_t tok0 = u * pair_tokens, ntok = min(pair_tokens, tokens - tok0);
+    // it runs only if it holds a token of a small request (of its larger ones, a few at most, none is empty)
+    int32_t ktiles = 0;
+    for (int32_t t = tok0; t < tok0 + ntok && ktiles == 0;) {
+      const int i = last_not_above(s_start, p.B, t);
+      if (s_start[i + 1] - s_start[i] <= Tt) ktiles = ptiles;
+      t = s_start[i + 1];
+    }
+    const int64_t cost = store_unit(p, u, {-1, tok0, ntok, ktiles, ptiles, -1, 0, 0});
+    if (u == first[0]) cost0[0] = cost;
+    sum[0] += cost;
+  }
+  int b = -1;
+#pragma unroll 1
+  for (int u = first[1]; u < behind[1]; ++u) {
+    const int32_t w = u - np;
+    if (b < 0 || s_unit[b + 1] <= w) {
+      // a step of single tokens has one unit for each request
+      const bool same = w < p.B && s_unit[w] == w && s_unit[w + 1] > w;
+      b = same ? w : last_not_above(s_unit, p.B, w);
+    }
+    const int32_t c = p.cached[b], f = s_start[b + 1] - s_start[b], i0 = (w - s_unit[b]) * pair_tokens;
+    const int32_t ntok = min(pair_tokens, f - i0), pos0 = c + i0, len = c + f;
     const bool small = shared && f <= Tt;
-    wf_batch_unit r;
-    r.req = b;
-    r.tok0 = s_start[b] + i0;
-    r.ntok = min(pair_tokens, f - i0);
-    r.pos0 = c + i0;
-    r.len = c + f;
-    const uint32_t last = uint32_t(r.pos0 + r.ntok - 1), G = uint32_t(p.block_tokens);
-    const int32_t end = int32_t(min(uint32_t(r.len), (last / G + 1) * G));  // the product is at most last + G
-    r.ptiles = small ? -1 : ptiles;
-    r.ktiles = ((end + 127) >> 7) + (small ? 0 : ptiles);
-    r.cbase = r.ntok <= Tt ? s_ctok[b] : -1;
-    p.units[np + u] = r;
+    const uint32_t last = uint32_t(pos0 + ntok - 1), G = uint32_t(p.block_tokens);
+    const uint32_t seen = G == 1 ? last + 1 : (last / G + 1) * G;  // at most last + G
+    const int32_t end = int32_t(min(uint32_t(len), seen));
+    const int64_t cost = store_unit(p, u, {b, s_start[b] + i0, ntok, ((end + 127) >> 7) + (small ? 0 : ptiles),
+                                           small ? -1 : ptiles, ntok <= Tt ? s_ctok[b] : -1, pos0, len});
+    if (u == first[1]) cost0[1] = cost;
+    sum[1] += cost;
   }
-  __syncthreads();
-  // prefix units run only where a tile holds a token of a small request
-  if (shared)
-    for (int b = b0; b < b1; ++b) {
-      const int32_t s = s_start[b], f = s_start[b + 1] - s;
-      if (f > 0 && f <= Tt)
-        for (int u = s / pair_tokens; u <= (s + f - 1) / pair_tokens; ++u) p.units[u].ktiles = ptiles;
+  block_scan<2, kThreads>(sum, all_costs, scratch);
+  const int64_t carry = all_costs[0] + all_costs[1];
+  sum[1] += all_costs[0];
+#pragma unroll
+  for (int kind = 0; kind < 2; ++kind) {
+    int64_t at = sum[kind];
+    for (int u = first[kind]; u < behind[kind]; ++u) {
+      p.pre[u] = at;
+      at += u == first[kind] ? cost0[kind] : unit_cost(p, p.units[u].ntok, p.units[u].ktiles);
     }
-  __syncthreads();
-  int64_t carry = 0;
-  for (int u0 = 0; u0 < np + own; u0 += kThreads) {
-    const int u = u0 + tid;
-    int64_t cost[1] = {0}, sum[1];
-    if (u < np + own) {
-      const int32_t kt = p.units[u].ktiles, nt = p.units[u].ntok;
-      if (kt > 0)
-        cost[0] = (int64_t(kt) << (nt > Tt ? WF_BATCH_PAIR_SHIFT : WF_BATCH_SINGLE_SHIFT)) + WF_BATCH_UNIT_COST;
-    }
-    block_scan<1, kThreads>(cost, sum, scratch);
-    if (u < np + own) p.pre[u] = carry + cost[0];
-    carry += sum[0];
   }
   __shared__ int64_t s_share;
   __shared__ double s_rcp;
   if (tid == 0) {
-    p.pre[np + own] = carry;
+    p.pre[units] = carry;
     wf_batch_hdr h{};
     h.fingerprint = p.fingerprint;
     h.tokens = tokens;
-    h.units = np + own;
+    h.units = units;
     h.prefix_units = np;
     h.prefix_len = prefix;
     h.ctoks = sum_ctok(total);
@@ -323,14 +341,19 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesPara
   // the unit that holds the beginning of each share, found from the units' side
   const int64_t share = s_share;
   const double rcp = s_rcp;
-  for (int u = tid; u < np + own; u += kThreads) {
-    const int64_t at = p.pre[u], end = p.pre[u + 1];
-    for (int h = 0; h < p.kv_heads; ++h) {
-      const int64_t s = h * carry + at, e = h * carry + end;
-      int c = int(double(s) * rcp);  // first share that begins at or behind s: within one of the quotient
-      while (c > 0 && (c - 1) * share >= s) --c;
-      while (c * share < s) ++c;
-      for (; c * share < e; ++c) p.starts[c] = {h, u};
+#pragma unroll 1
+  for (int kind = 0; kind < 2; ++kind) {
+    int64_t end = kind ? sum[1] : sum[0];
+    for (int u = kind ? first[1] : first[0]; u < (kind ? behind[1] : behind[0]); ++u) {
+      const int64_t at = end;
+      end = p.pre[u + 1];
+      for (int h = 0; h < p.kv_heads; ++h) {
+        const int64_t s = h * carry + at, e = h * carry + end;
+        int c = int(double(s) * rcp);  // first share that begins at or behind s: within one of the quotient
+        while (c > 0 && (c - 1) * share >= s) --c;
+        while (c * share < s) ++c;
+        for (; c * share < e; ++c) p.starts[c] = {h, u};
+      }
     }
   }
 }
@@ -531,10 +554,10 @@ extern "C" wf_status wf_batch_tables(const wf_batch_desc* desc, const int32_t* c
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // Blocks of 256 or 1024 threads.  A small block starts and scans sooner, a
-  // large one has a thread for every request: 5 requests 4.9 us with 256 and
-  // 5.8 us with 1024, 64 requests 5.0 and 6.2 us; 256 requests 7.2 and 7.0 us,
-  // 512 9.8 and 8.2 us, 1024 14.4 and 12.0 us, 8192 119 and 58 us.
-  return p.B <= 128 ? launch_tables<256>(p, st) : launch_tables<1024>(p, st);
+  // large one has a thread for every request (a call in a graph): 5 requests 4.5
+  // us with 256 and 5.5 us with 1024, 256 requests 5.1 and 6.2 us, 512 6.5 and
+  // 6.8 us, 1024 9.8 and 8.0 us, 8192 115 and 51 us.
+  return p.B <= 512 ? launch_tables<256>(p, st) : launch_tables<1024>(p, st);
 }
 
 extern "C" wf_status wf_batch_status(const void* plan, wf_stream_t stream, int32_t* detail) {
