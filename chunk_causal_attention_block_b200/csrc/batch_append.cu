@@ -51,6 +51,7 @@ __device__ __forceinline__ uint32_t rotate_bf16x2(uint32_t xy, float c, float s)
 // kVec: 16-byte columns of a row (D / 8).
 template <int kVec, bool kRope>
 __global__ void __launch_bounds__(kMaxThreads, 3) batch_append_kernel(const AppendParams p) {
+  cudaGridDependencySynchronize();
   if (p.hdr->fingerprint != p.fingerprint) return;
   const int tokens = p.hdr->tokens;
   const int col = threadIdx.x % kVec, line = threadIdx.x / kVec;
@@ -63,8 +64,8 @@ __global__ void __launch_bounds__(kMaxThreads, 3) batch_append_kernel(const Appe
     float4 cs0, cs1;
     if (kRope) {
       const float4* r = p.rope + (t * kVec + col) * 2;
-      cs0 = __ldg(r);
-      cs1 = __ldg(r + 1);
+      cs0 = r[0];
+      cs1 = r[1];
     }
     for (int r0 = first; r0 < rows; r0 += p.slots * kInFlight) {
       uint4 x[kInFlight];
@@ -142,16 +143,7 @@ extern "C" wf_status wf_batch_append(const wf_batch_desc* desc, const void* plan
   const int threads = vec * p.slots * per_block;
   const unsigned blocks = unsigned(std::min((desc->max_tokens + per_block - 1) / per_block, L.ctas * 32));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (desc->head_dim == 128) {
-    if (rope)
-      batch_append_kernel<16, true><<<blocks, threads, 0, s>>>(p);
-    else
-      batch_append_kernel<16, false><<<blocks, threads, 0, s>>>(p);
-  } else {
-    if (rope)
-      batch_append_kernel<8, true><<<blocks, threads, 0, s>>>(p);
-    else
-      batch_append_kernel<8, false><<<blocks, threads, 0, s>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
+  void (*kernel)(AppendParams) = desc->head_dim == 128 ? (rope ? batch_append_kernel<16, true> : batch_append_kernel<16, false>)
+                                                       : (rope ? batch_append_kernel<8, true> : batch_append_kernel<8, false>);
+  return wf::launch_early(kernel, blocks, unsigned(threads), 0, s, p);
 }

@@ -387,9 +387,9 @@ __device__ __forceinline__ bool load_unit(const Params& p, const Share& x, int32
                                           int64_t& s) {
   if (unit >= x.units) return false;
   const int4* src = reinterpret_cast<const int4*>(p.units + unit);
-  reinterpret_cast<int4*>(&r)[0] = __ldg(src);
-  reinterpret_cast<int4*>(&r)[1] = __ldg(src + 1);
-  s = int64_t(head) * x.head_cost + __ldg(p.pre + unit);
+  reinterpret_cast<int4*>(&r)[0] = src[0];
+  reinterpret_cast<int4*>(&r)[1] = src[1];
+  s = int64_t(head) * x.head_cost + p.pre[unit];
   return true;
 }
 
@@ -507,7 +507,7 @@ __device__ __forceinline__ KeyTile key_tile(const Params& p, const Item& x, int3
   const int32_t pg = int32_t(threadIdx.x & 31);
   const int32_t* list = own ? p.table + x.req * p.cols : p.prefix_table;
   const int32_t first = ((own ? j - x.ptiles : j) * 128) >> p.page_shift;
-  k.page = pg << p.page_shift < valid ? __ldg(list + first + pg) : 0;
+  k.page = pg << p.page_shift < valid ? list[first + pg] : 0;
   return k;
 }
 
@@ -1218,7 +1218,7 @@ __device__ __forceinline__ void softmax_role(const Shared<D>& sh, const Params& 
     if (dest == kCut) {
       out_row += (pair ? other : t) * 128 + row;
     } else if (dest == kMainPrefix) {
-      const int32_t ct = live ? __ldg(p.ctok + tok) : -1;
+      const int32_t ct = live ? p.ctok[tok] : -1;
       // a larger request's row in a shared tile has its prefix elsewhere
       out_row = ct < 0 ? -1 : out_row + (pair ? 0 : t * half_rows) + int64_t(ct) * p.H + row_head;
     } else {
@@ -1256,6 +1256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const Shared<D> sh{raw, (raw + C::kSmall + 1023) & ~1023u};
   if (sh.tiles + C::kTiles > raw + C::kSmemBytes) {  // dynamic shared memory not on a 1024-byte boundary: never seen
+    cudaGridDependencySynchronize();
     if (threadIdx.x == 0) p.status->code = WF_ERR_ALIGNMENT;
     return;
   }
@@ -1282,18 +1283,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
-  } else if (warp == 10) {
-    share = first_share(p);
-    load_unit(p, share, share.head, share.unit + lane, unit, unit_at);
-  }
-  // the merging kernel may come onto this SM as soon as this block leaves it
-  cudaTriggerProgrammaticLaunchCompletion();
-  if (blockIdx.x == 0 && threadIdx.x == 0 && p.hdr->fingerprint != p.fingerprint)
-    p.status->code = WF_ERR_PLAN;  // not built, or for another description: the scheduler finds no work
-  if (warp == 8) {
+  } else if (warp == 8) {
     tmem_alloc(sh.base + Shared<D>::kTmemAt, kTmemCols);
     tmem_relinquish();
   }
+  // Launched while the stream's previous kernel may still run: nothing before
+  // this line reads or writes global memory.
+  cudaGridDependencySynchronize();
+  // The merging kernel may come onto this SM as soon as this block leaves it.
+  // (Behind the wait: it reads the plan before it waits itself.)
+  cudaTriggerProgrammaticLaunchCompletion();
+  if (warp == 10) {
+    share = first_share(p);
+    load_unit(p, share, share.head, share.unit + lane, unit, unit_at);
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.hdr->fingerprint != p.fingerprint)
+    p.status->code = WF_ERR_PLAN;  // not built, or for another description: the scheduler finds no work
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1568,25 +1573,13 @@ wf_status launch(const wf_batch_desc* d, const BatchLayout& L, const Params& p, 
       !make_pool_map(&tk, k_pool, pool, d->num_kv_heads, D, d->page_tokens) ||
       !make_pool_map(&tv, v_pool, pool, d->num_kv_heads, D, d->page_tokens))
     return WF_ERR_CUDA;
-  batch_attn_kernel<D><<<L.ctas, kThreads, Cfg<D>::kSmemBytes, stream>>>(tq, tn, tk, tv, p);
-  if (cudaGetLastError() != cudaSuccess) return WF_ERR_CUDA;
+  const wf_status launched =
+      launch_early(batch_attn_kernel<D>, unsigned(L.ctas), kThreads, Cfg<D>::kSmemBytes, stream, tq, tn, tk, tv, p);
+  if (launched != WF_OK) return launched;
   // as many blocks as the rows that may have to be merged fill, or as run at once a few times over
   const int64_t rows = std::max(L.max_ctok * d->num_heads, d->max_tokens > L.tile_tokens ? int64_t(L.ctas) * 256 : 0);
   const int64_t blocks = (rows + kCombineRows - 1) / kCombineRows, most = int64_t(L.ctas) * 16;
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(blocks < most ? blocks : most));
-  cfg.blockDim = dim3(kCombineThreads);
-  cfg.stream = stream;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, batch_combine_kernel<D>, p) != cudaSuccess) {
-    cudaGetLastError();
-    return WF_ERR_CUDA;
-  }
-  return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
+  return launch_early(batch_combine_kernel<D>, unsigned(blocks < most ? blocks : most), kCombineThreads, 0, stream, p);
 }
 
 bool misaligned(const void* ptr) { return reinterpret_cast<uintptr_t>(ptr) % 16 != 0; }

@@ -148,20 +148,21 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesPara
   int32_t* s_unit = s_ctok + p.B;       // [B + 1] first own unit
   __shared__ int64_t scratch[3 * (kThreads / 32 + 1)];
 
+  cudaGridDependencySynchronize();
   const int tid = threadIdx.x;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
   const int Tt = p.tile_tokens;
-  const int32_t prefix = p.prefix_len ? __ldg(p.prefix_len) : 0;
-  const int32_t head = __ldg(p.free_head);
+  const int32_t prefix = p.prefix_len ? *p.prefix_len : 0;
+  const int32_t head = *p.free_head;
 
   Sums v{};
   int64_t total[3];
   int bad = 0;  // 1: invalid, 2: does not fit
   for (int b = b0; b < b1; ++b) {
-    const int32_t c = __ldg(p.cached + b), f = __ldg(p.fresh + b);
+    const int32_t c = p.cached[b], f = p.fresh[b];
     const int32_t least = c < 0 ? 0 : ceil_shift(c, p.page_shift);
-    const int32_t h = p.held ? __ldg(p.held + b) : least;
+    const int32_t h = p.held ? p.held[b] : least;
     if (c < 0 || f < 0 || h < least) {
       bad |= 1;
       continue;
@@ -200,8 +201,8 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(const TablesPara
   const bool shared = prefix > 0 && sum_small(total) >= 2;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    const int32_t c = __ldg(p.cached + b), f = __ldg(p.fresh + b);
-    const int32_t h = p.held ? __ldg(p.held + b) : ceil_shift(c, p.page_shift);
+    const int32_t c = p.cached[b], f = p.fresh[b];
+    const int32_t h = p.held ? p.held[b] : ceil_shift(c, p.page_shift);
     const int32_t n = max(h, ceil_shift(int64_t(c) + f, p.page_shift));
     s_start[b] = int32_t(sum_tokens(v.w));
     s_first[b] = int32_t(sum_pages(v.w));
@@ -380,8 +381,7 @@ wf_status launch_tables(const TablesParams& p, cudaStream_t stream) {
   const int token_blocks = (p.max_tokens + kThreads - 1) / kThreads;
   const int most = 147 * (1024 / kThreads);
   const int blocks = 1 + (token_blocks < most ? token_blocks : most);
-  batch_tables_kernel<kThreads><<<blocks, kThreads, smem, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? WF_OK : WF_ERR_CUDA;
+  return wf::launch_early(batch_tables_kernel<kThreads>, blocks, kThreads, smem, stream, p);
 }
 
 // SM count of the current device, asked for once per device.

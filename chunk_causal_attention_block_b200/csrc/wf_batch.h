@@ -83,4 +83,31 @@ BatchLayout batch_layout(const wf_batch_desc* d);
 // Whether ptr is memory of the current device: elsewhere a kernel would fault on it.
 bool on_current_device(const void* ptr);
 
+#ifdef __CUDACC__
+// Launches a kernel that may start while the kernel before it in the stream
+// still runs, and that touches no global memory before it has called
+// cudaGridDependencySynchronize (but what older kernels than that one wrote).
+// Such kernels read with plain loads: __ldg is for data that nobody writes while
+// the kernel runs, which here begins before the wait ends.
+// Saves the gap between two kernels, 1.5 to 2 us: one token's attention 12.3 ->
+// 10.7 us a call, 64 decoding requests 53.7 -> 51.7 us.
+template <typename... Params, typename... Args>
+wf_status launch_early(void (*kernel)(Params...), unsigned blocks, unsigned threads, size_t smem, cudaStream_t stream,
+                       const Args&... args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, Params(args)...) == cudaSuccess) return WF_OK;
+  cudaGetLastError();
+  return WF_ERR_CUDA;
+}
+#endif
+
 }  // namespace wf
