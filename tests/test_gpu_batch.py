@@ -380,3 +380,88 @@ def test_an_expired_wait_in_a_fresh_workspace_leaves_other_rows_alone(monkeypatc
         monkeypatch.delenv("WF_WAIT_TIMEOUT_MS")
         assert code == wf.WF_ERR_DEVICE_TIMEOUT
         assert (s.out[s.T:] == SENTINEL).all() and (s.lse[:, s.T:] == SENTINEL).all()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("D,num_ctas", [(128, 0), (64, 23)])
+def test_calls_wait_for_what_is_before_them_in_the_stream(D, num_ctas, captured):
+    # kernels, copies, fills and a join with another stream stand right before each call, and a reader right behind
+    s = Step([200, 3, 900], [1, 9, 300], prefix=500, D=D, num_ctas=num_ctas)
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    s.stream = side
+    table = s.d["block_table"].clone()
+    inputs, want = [], []
+    for i in range(2):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(100 + i)
+        inputs.append([torch.randn(x.shape, generator=g, device="cuda").to(torch.bfloat16) for x in (s.q, s.k, s.v)] +
+                      [torch.tensor([[1, 9, 300], [5, 0, 130]][i], dtype=torch.int32, device="cuda")])
+    busy, pool = torch.zeros(1 << 24, device="cuda"), (s.k_pool.clone(), s.v_pool.clone())
+
+    def step(new, results):
+        for dst, src in zip((s.k_pool, s.v_pool), pool):
+            dst.copy_(src)
+        busy.add_(1)
+        s.out.fill_(SENTINEL)
+        for name, x in zip(("q", "k", "v"), new):
+            getattr(s, name).copy_(x)
+        s.d["block_table"].copy_(table)
+        s.d["slot_map"].zero_()
+        s.d["fresh"].copy_(new[3])
+        s.tables()
+        results.append(s.d["slot_map"].clone())
+        s.k.copy_(new[1])
+        s.append()
+        other.wait_stream(side)
+        with torch.cuda.stream(other):
+            busy.mul_(0.5)
+            s.lse.fill_(SENTINEL)
+        side.wait_stream(other)
+        s.attend()
+        results.append(s.out.clone())
+        results.append(s.lse.clone())
+        s.q_rot.zero_()
+        s.d["plan"][256:].zero_()  # the next step builds another
+
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for i in range(2):
+            want.append([])
+            step(inputs[i], want[i])
+            torch.cuda.synchronize()
+            assert not torch.isnan(want[i][1].float()).any() and not torch.equal(want[i][1], torch.full_like(s.out, SENTINEL))
+        assert not torch.equal(want[0][1], want[1][1])
+        got = [[] for _ in range(8)]
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                for i in range(8):
+                    step(inputs[i % 2], got[i])
+            for _ in range(3):
+                graph.replay()
+        else:
+            for i in range(8):
+                step(inputs[i % 2], got[i])
+    torch.cuda.synchronize()
+    for i in range(8):
+        for a, b in zip(got[i], want[i % 2]):
+            assert torch.equal(a, b), i
+
+
+def test_a_call_may_be_the_first_of_a_graph_and_follow_a_copy_alone():
+    s = Step([200, 3], [1, 9], prefix=500).run()
+    s.check_attention()
+    out, host = s.out.clone(), s.q_rot.cpu().pin_memory()
+    side = torch.cuda.Stream()
+    s.stream = side
+    for before in (lambda: None, lambda: s.q_rot.copy_(host, non_blocking=True), lambda: s.out.zero_()):
+        for call in (s.tables, s.append, s.attend):
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                before()
+                call()
+            if call == s.attend:
+                graph.replay()
+            torch.cuda.synchronize()
+        assert torch.equal(s.out[:s.T], out[:s.T])
