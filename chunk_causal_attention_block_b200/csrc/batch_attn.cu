@@ -1390,8 +1390,19 @@ __device__ __forceinline__ void merge_row(const Params& p, const Line& line, boo
     const int i = base + g;
     int64_t row = -1;
     if (i < n) row = i < a.n ? part_row(p, line, a, i, ct, head) : part_row(p, line, b, i - a.n, ct, head);
-    // (a part that saw no key has no O row: its weight is 0 and it is not read)
     const float x = row >= 0 ? p.part_lse[row] : -INFINITY;
+    // the first O rows are on their way before their weights are known: one latency instead of two
+    float4 o[kAhead][Q];
+    auto load = [&](int k) {
+#pragma unroll
+      for (int c = 0; c < kAhead; ++c) {
+        const int64_t r = __shfl_sync(0xffffffffu, row, group + k + c);
+        const float4* src = reinterpret_cast<const float4*>(p.part_o + r * D) + g;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) o[c][q] = r >= 0 ? __ldcs(src + 8 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    };
+    load(0);
     float mx = x;
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
@@ -1409,25 +1420,20 @@ __device__ __forceinline__ void merge_row(const Params& p, const Line& line, boo
     }
 #pragma unroll 1
     for (int k = 0; k < 8 && base + k < most; k += kAhead) {
-      float4 o[kAhead][Q];
-      float wk[kAhead];
+      if (k > 0) load(k);
 #pragma unroll
       for (int c = 0; c < kAhead; ++c) {
-        wk[c] = __shfl_sync(0xffffffffu, w, group + k + c);
-        const float4* src =
-            reinterpret_cast<const float4*>(p.part_o + __shfl_sync(0xffffffffu, row, group + k + c) * D) + g;
+        const float wk = __shfl_sync(0xffffffffu, w, group + k + c);
+        // (a part that saw no key has no O row: whatever lies there is not used)
 #pragma unroll
-        for (int q = 0; q < Q; ++q) o[c][q] = wk[c] != 0.f ? __ldcs(src + 8 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q = 0; q < Q; ++q)
+          if (wk != 0.f) {
+            acc[q].x = fmaf(wk, o[c][q].x, acc[q].x);
+            acc[q].y = fmaf(wk, o[c][q].y, acc[q].y);
+            acc[q].z = fmaf(wk, o[c][q].z, acc[q].z);
+            acc[q].w = fmaf(wk, o[c][q].w, acc[q].w);
+          }
       }
-#pragma unroll
-      for (int c = 0; c < kAhead; ++c)
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-          acc[q].x = fmaf(wk[c], o[c][q].x, acc[q].x);
-          acc[q].y = fmaf(wk[c], o[c][q].y, acc[q].y);
-          acc[q].z = fmaf(wk[c], o[c][q].z, acc[q].z);
-          acc[q].w = fmaf(wk[c], o[c][q].w, acc[q].w);
-        }
     }
   }
   if (!on) return;
