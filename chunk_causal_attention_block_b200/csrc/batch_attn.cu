@@ -991,24 +991,35 @@ __device__ __forceinline__ bool narrow_tile(const Shared<D>& sh, const Params& p
 }
 
 // A narrow item's rows out of O^T: lane = dim, so a warp stores 32 dims of a
-// row at once.  dst: of the lane's row (nullptr: none); scale likewise.
+// row at once.  row: output or partial row of the lane's row (-1: none; no
+// memory holds 2^31 of them); scale likewise.
 template <int D>
-__device__ __forceinline__ void store_columns(uint32_t o_tm, uint8_t* dst, bool as_bf16, float scale, int rows) {
+__device__ __forceinline__ void store_columns(const Params& p, uint32_t o_tm, int32_t row, bool direct, float scale,
+                                              int rows) {
   const int dim = threadIdx.x & 127;
+  if (dim >= D) return;  // (whole warps)
 #pragma unroll 1
   for (int c = 0; c < rows; c += 4) {
     uint32_t r[4];
+    int32_t to[4];
+    float o[4];
     tmem_ld4(o_tm + c, r);
-    tmem_wait_ld();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      uint8_t* to = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(dst), c + i));
-      const float o = __uint_as_float(r[i]) * __shfl_sync(0xffffffffu, scale, c + i);
-      if (to == nullptr || dim >= D) continue;
-      if (as_bf16)
-        reinterpret_cast<__nv_bfloat16*>(to)[dim] = __float2bfloat16_rn(o);
-      else
-        reinterpret_cast<float*>(to)[dim] = o;
+      to[i] = __shfl_sync(0xffffffffu, row, c + i);
+      o[i] = __shfl_sync(0xffffffffu, scale, c + i);
+    }
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] *= __uint_as_float(r[i]);
+    if (direct) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (to[i] >= 0) p.out[int64_t(to[i]) * D + dim] = __float2bfloat16_rn(o[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (to[i] >= 0) p.part_o[int64_t(to[i]) * D + dim] = o[i];
     }
   }
 }
@@ -1072,8 +1083,9 @@ __device__ __forceinline__ void softmax_role(const Shared<D>& sh, const Params& 
   uint32_t s_phase = 0, o_phase = 0, x_phase = 0, ot = 0;
   Pending pend;
   auto store_pending = [&](float sum) {
-    uint8_t* dst = row_out<D>(p, pend.direct, pend.row, pend.lse, pend.m, sum, warp == 0, true);
-    store_columns<D>(o_tm + kNarrow * (ot ^ 1), dst, pend.direct, sum != 0.f ? __frcp_rn(sum) : 0.f, pend.rows);
+    row_out<D>(p, pend.direct, pend.row, pend.lse, pend.m, sum, warp == 0, true);
+    store_columns<D>(p, o_tm + kNarrow * (ot ^ 1), int32_t(pend.row), pend.direct, sum != 0.f ? __frcp_rn(sum) : 0.f,
+                     pend.rows);
     pend.on = false;
   };
   for (int it = 0;; ++it) {
