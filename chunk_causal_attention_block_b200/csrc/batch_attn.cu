@@ -37,8 +37,8 @@
 // each, 32760 shared, 12 heads: 250 us, 1.50 GB, 6.0 TB/s).  Long proposals:
 // the exponentials and MMAs of the two streams together, under the power limit
 // (2 x 4680 tokens over 42120 keys, 12 heads: 2.0-2.3 ms, 1.1-1.2 PFLOP/s of
-// visible pairs).  A few rows: latency (one token over 334 keys: 15 us, most
-// of it the host's).
+// visible pairs).  A few rows: latency (one token over 334 keys: 10 us, 4 of
+// them the merging's).
 //
 // Warp roles (384 threads):
 //   warps 0-3, 4-7  softmax of stream 0 and 1
