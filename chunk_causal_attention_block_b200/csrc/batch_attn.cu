@@ -113,7 +113,8 @@ struct Params {
   __nv_bfloat16* out;
   float* lse;
   wf_dev_status* status;
-  float* part_o;    // partial rows: [prefix, own][key parity][ctok][H], then [CTA][head, tail][row tile or key parity][128]
+  // partial rows: [prefix, own][key parity][ctok][H], then [CTA][head, tail][row tile or key parity][128]
+  float* part_o;
   float* part_lse;
   Cut* cuts;        // per CTA
   int64_t main_rows;
@@ -760,7 +761,8 @@ __device__ __forceinline__ void mma_issuer(const Shared<D>& sh, const Params& p,
       if (elect_one()) {
         const uint32_t acc = pv2 & kPvFirst ? 0u : 1u;
         if (pv2 & kPvNarrow)
-          issue_ot_slice<D, 0>(tmem + 256 + 128 * t + kNarrow * ((ot >> t) & 1), vd, smem_desc_sw128(sh.p_tile(t), 16, kAtom), acc);
+          issue_ot_slice<D, 0>(tmem + 256 + 128 * t + kNarrow * ((ot >> t) & 1), vd,
+                               smem_desc_sw128(sh.p_tile(t), 16, kAtom), acc);
         else
           issue_pv_slice<D, 0>(tmem + 256 + 128 * t, tmem + 128 * t, vd, acc);
         if (pv2 & kPvLast) mma_commit(sh.bar(C::kOFull + t));
@@ -1357,8 +1359,8 @@ struct Parts {
   int32_t half, row;  // of a two-tile unit: the row's tile; the row in its tile
 };
 
-__device__ __forceinline__ Parts parts_of(const Params& p, const Line& line, const wf_batch_unit& u, int64_t s, int32_t tok_i,
-                                          int32_t row_head) {
+__device__ __forceinline__ Parts parts_of(const Params& p, const Line& line, const wf_batch_unit& u, int64_t s,
+                                          int32_t tok_i, int32_t row_head) {
   Parts q;
   q.s = s;
   q.pair = u.ntok > p.tile_tokens;
@@ -1375,7 +1377,8 @@ __device__ __forceinline__ Parts parts_of(const Params& p, const Line& line, con
 }
 
 // Row index of part i, or -1 if that share holds none of the unit's tiles.
-__device__ __forceinline__ int64_t part_row(const Params& p, const Line& line, const Parts& q, int i, int32_t ct, int32_t head) {
+__device__ __forceinline__ int64_t part_row(const Params& p, const Line& line, const Parts& q, int i, int32_t ct,
+                                            int32_t head) {
   const int half = q.pair ? q.half : i & 1;
   if (!q.cut) return main_row(p, q.own, q.pair ? 0 : half, ct, head);
   const int c = q.c0 + (q.pair ? i : i >> 1);

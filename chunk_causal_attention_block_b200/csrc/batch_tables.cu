@@ -99,7 +99,7 @@ __device__ void block_scan(int64_t (&v)[N], int64_t (&total)[N], int64_t* scratc
 struct Sums {
   int64_t w[3];
   __device__ __forceinline__ void add(int32_t f, int32_t new_pages, int32_t tile_tokens) {
-    const int32_t tiles = f <= tile_tokens ? f > 0 : (f + tile_tokens - 1) / tile_tokens;  // (a division takes 30 instructions)
+    const int32_t tiles = f <= tile_tokens ? f > 0 : (f + tile_tokens - 1) / tile_tokens;  // (mostly no division)
     w[0] += f;
     w[1] += (int64_t(new_pages) << 24) + ((tiles & 1) ? f - (tiles - 1) * tile_tokens : 0);
     w[2] += (int64_t((tiles + 1) / 2) << 16) + (f > 0 && f <= tile_tokens);
@@ -495,8 +495,8 @@ extern "C" wf_status wf_batch_tables(const wf_batch_desc* desc, const int32_t* c
                                      int32_t* positions, void* plan, size_t plan_bytes, wf_stream_t stream) {
   const wf::BatchLayout L = wf::batch_layout(desc);
   if (L.error != WF_OK) return L.error;
-  if (!cached || !fresh || (!free_pages && num_free > 0) || !free_head || !free_head_out || !block_table || !token_start || !slot_map ||
-      !positions || !plan || num_free < 0)
+  if (!cached || !fresh || (!free_pages && num_free > 0) || !free_head || !free_head_out || !block_table ||
+      !token_start || !slot_map || !positions || !plan || num_free < 0)
     return WF_ERR_INVALID_ARG;
   if (desc->max_prefix_pages > 0 && !prefix_len) return WF_ERR_INVALID_ARG;
   if ((held == nullptr) != (held_out == nullptr)) return WF_ERR_INVALID_ARG;

@@ -148,7 +148,8 @@ PyObject* tables(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
 }
 
 PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
-  static const char* const names[] = {"desc", "plan", "slot_map", "rope", "q", "k", "v", "q_rot", "k_pool", "v_pool", "stream"};
+  static const char* const names[] = {"desc", "plan", "slot_map", "rope", "q", "k", "v", "q_rot", "k_pool", "v_pool",
+                                      "stream"};
   return guarded(names, args, nargs, [](const wf_batch_desc& d, Reader r) {
     void* plan = r.plan(1);
     // a step may hold fewer tokens than max_tokens: only the device knows, so room for all is asked for

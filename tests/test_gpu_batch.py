@@ -465,3 +465,52 @@ def test_a_call_may_be_the_first_of_a_graph_and_follow_a_copy_alone():
                 graph.replay()
             torch.cuda.synchronize()
         assert torch.equal(s.out[:s.T], out[:s.T])
+
+
+def test_a_step_that_needs_no_page_runs_without_free_ones():
+    s = Step([20, 3], [2, 5], prefix=50, held=[2, 1])
+    s.d["free_pages"] = torch.zeros(0, dtype=torch.int32, device="cuda")
+    s.free_head = 0
+    s.d["free_head"].zero_()
+    s.run()
+    s.check_tables()
+    s.check_attention()
+    s.d["held"].copy_(torch.tensor([2, 0], dtype=torch.int32))
+    s.tables()
+    assert wf.wf_batch_status(s.d["plan"], s.stream) == wf.WF_ERR_INVALID_ARG  # fewer held than the cached tokens fill
+    s.d["held"].copy_(torch.tensor([2, 1], dtype=torch.int32))
+    s.d["fresh"].copy_(torch.tensor([2, 14], dtype=torch.int32))
+    s.tables()
+    assert wf.wf_batch_status(s.d["plan"], s.stream) == wf.WF_ERR_CAPACITY
+
+
+def test_two_threads_call_at_once():
+    import threading
+    steps = [Step([900, 20], [1, 30], prefix=1500), Step([5, 60, 7], [200, 1, 2], prefix=300, D=64, H=6, Hkv=3)]
+    want = []
+    for s in steps:
+        s.run()
+        s.check_attention()
+        want.append((s.out.clone(), s.lse.clone(), s.d["slot_map"].clone()))
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(s):
+        try:
+            torch.cuda.set_device(0)
+            s.stream = torch.cuda.Stream()
+            for _ in range(200):
+                s.run()
+            s.stream.synchronize()
+        except Exception as e:  # noqa: BLE001 (seen by the test below)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(s,)) for s in steps]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for s, w in zip(steps, want):
+        for got, x in zip((s.out, s.lse, s.d["slot_map"]), w):
+            assert torch.equal(got, x)
