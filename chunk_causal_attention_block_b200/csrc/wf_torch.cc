@@ -10,9 +10,9 @@
 // us, append of 32 tokens 12.2 -> 8.0 us, attention of one token 16.3 -> 11.1
 // us.)
 //
-// An argument is a CUDA tensor, dense, of the element size and at least the
-// size that the call may touch and on the device of the plan; None; or a raw
-// address, which its owner vouches for.
+// An argument is a CUDA tensor, dense, of the type and at least the size that
+// the call may touch and on the device of the plan; None; or a raw address,
+// which its owner vouches for.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -36,6 +36,8 @@ struct Refused {
 };
 
 constexpr int kAnyDevice = -1;
+constexpr auto kInt = at::ScalarType::Int, kFloat = at::ScalarType::Float, kBf16 = at::ScalarType::BFloat16;
+constexpr auto kBytes = at::ScalarType::Undefined;  // memory without a type of its own: elements of one byte
 
 // Turns arguments into addresses.
 struct Reader {
@@ -47,23 +49,24 @@ struct Reader {
 
   // The call's plan settles the device of all its tensors.
   void* plan(int i) {
-    void* p = address(i, 0, 1);
+    void* p = address(i, 0, kBytes);
     if (const at::Tensor* t = tensor(args[i])) device = t->get_device();
     return p;
   }
 
-  void* address(int i, int64_t n, int64_t size) const {
+  void* address(int i, int64_t n, at::ScalarType type) const {
     PyObject* x = args[i];
     if (x == Py_None) return nullptr;
     if (const at::Tensor* t = tensor(x)) {
+      if (type == kBytes ? t->itemsize() != 1 : t->scalar_type() != type)
+        throw Refused{std::string(names[i]) + " is of type " + c10::toString(t->scalar_type()) + " where " +
+                      (type == kBytes ? "bytes" : c10::toString(type)) + " is needed"};
       const bool dense = t->layout() == at::kStrided && t->is_contiguous();
-      if (dense && t->is_cuda() && int64_t(t->itemsize()) == size && t->numel() >= n &&
-          (device == kAnyDevice || t->get_device() == device))
+      if (dense && t->is_cuda() && t->numel() >= n && (device == kAnyDevice || t->get_device() == device))
         return t->data_ptr();
       std::ostringstream s;
-      s << names[i] << " has " << t->numel() << " elements of " << t->itemsize() << " bytes on " << t->device()
-        << (dense ? "" : ", not dense") << " where " << n << " of " << size << " are needed on "
-        << (device == kAnyDevice ? "a GPU" : "the plan's GPU");
+      s << names[i] << " has " << t->numel() << " elements on " << t->device() << (dense ? "" : ", not dense")
+        << " where " << n << " are needed on " << (device == kAnyDevice ? "a GPU" : "the plan's GPU");
       throw Refused{s.str()};
     }
     if (!PyLong_Check(x)) throw Refused{std::string(names[i]) + " is neither a tensor nor an address nor None"};
@@ -131,7 +134,7 @@ PyObject* tables(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
                                       "slot_map", "positions", "plan_bytes", "stream"};
   return guarded(names, args, nargs, [](const wf_batch_desc& d, Reader r) {
     void* plan = r.plan(1);
-    auto i32 = [&](int i, int64_t n) { return static_cast<int32_t*>(r.address(i, n, 4)); };
+    auto i32 = [&](int i, int64_t n) { return static_cast<int32_t*>(r.address(i, n, kInt)); };
     const int64_t B = d.max_requests, T = d.max_tokens;
     int32_t *cached = i32(2, B), *fresh = i32(3, B), *prefix_len = i32(4, 1), *held = i32(5, B);
     const int64_t num_free = r.number(7, 6, false);
@@ -139,7 +142,7 @@ PyObject* tables(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     int32_t *free_pages = i32(6, num_free), *head = i32(8, 1), *head_out = i32(9, 1), *held_out = i32(10, B);
     int32_t *table = i32(11, B * d.max_request_pages), *start = i32(12, B + 1), *slots = i32(13, T), *pos = i32(14, T);
     const int64_t plan_bytes = r.number(15, 1, true);
-    auto stream = static_cast<wf_stream_t>(r.address(16, 0, 1));
+    auto stream = static_cast<wf_stream_t>(r.address(16, 0, kBytes));
     return without_gil([&] {
       return g_tables(&d, cached, fresh, prefix_len, held, free_pages, int32_t(num_free), head, head_out, held_out, table,
                       start, slots, pos, plan, plan_bytes < 0 ? 0 : size_t(plan_bytes), stream);
@@ -155,11 +158,11 @@ PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     // a step may hold fewer tokens than max_tokens: only the device knows, so room for all is asked for
     const int64_t T = d.max_tokens, kv = int64_t(d.num_kv_heads) * d.head_dim, q_size = T * d.num_heads * d.head_dim;
     const int64_t pool = int64_t(d.pool_pages) * d.page_tokens * kv;
-    auto slots = static_cast<const int32_t*>(r.address(2, T, 4));
-    auto rope = static_cast<const float*>(r.address(3, T * d.head_dim, 4));
-    void *q = r.address(4, q_size, 2), *k = r.address(5, T * kv, 2), *v = r.address(6, T * kv, 2);
-    void *q_rot = r.address(7, q_size, 2), *k_pool = r.address(8, pool, 2), *v_pool = r.address(9, pool, 2);
-    auto stream = static_cast<wf_stream_t>(r.address(10, 0, 1));
+    auto slots = static_cast<const int32_t*>(r.address(2, T, kInt));
+    auto rope = static_cast<const float*>(r.address(3, T * d.head_dim, kFloat));
+    void *q = r.address(4, q_size, kBf16), *k = r.address(5, T * kv, kBf16), *v = r.address(6, T * kv, kBf16);
+    void *q_rot = r.address(7, q_size, kBf16), *k_pool = r.address(8, pool, kBf16), *v_pool = r.address(9, pool, kBf16);
+    auto stream = static_cast<wf_stream_t>(r.address(10, 0, kBytes));
     return without_gil([&] { return g_append(&d, plan, slots, rope, q, k, v, q_rot, k_pool, v_pool, stream); });
   });
 }
@@ -171,16 +174,16 @@ PyObject* attn(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     void* plan = r.plan(1);
     const int64_t T = d.max_tokens, kv = int64_t(d.num_kv_heads) * d.head_dim, q_size = T * d.num_heads * d.head_dim;
     const int64_t pool = int64_t(d.pool_pages) * d.page_tokens * kv;
-    auto table = static_cast<const int32_t*>(r.address(2, int64_t(d.max_requests) * d.max_request_pages, 4));
-    auto prefix = static_cast<const int32_t*>(r.address(3, d.max_prefix_pages, 4));
-    void *q = r.address(4, q_size, 2), *k_pool = r.address(5, pool, 2), *v_pool = r.address(6, pool, 2);
-    void* out = r.address(7, q_size, 2);
-    auto lse = static_cast<float*>(r.address(8, T * d.num_heads, 4));
+    auto table = static_cast<const int32_t*>(r.address(2, int64_t(d.max_requests) * d.max_request_pages, kInt));
+    auto prefix = static_cast<const int32_t*>(r.address(3, d.max_prefix_pages, kInt));
+    void *q = r.address(4, q_size, kBf16), *k_pool = r.address(5, pool, kBf16), *v_pool = r.address(6, pool, kBf16);
+    void* out = r.address(7, q_size, kBf16);
+    auto lse = static_cast<float*>(r.address(8, T * d.num_heads, kFloat));
     const double scale = PyFloat_AsDouble(args[9]);
     if (scale == -1.0 && PyErr_Occurred()) throw Refused{"softmax_scale is not a number"};
-    void* workspace = r.address(10, 0, 1);
+    void* workspace = r.address(10, 0, kBytes);
     const int64_t bytes = r.number(11, 10, true);
-    auto stream = static_cast<wf_stream_t>(r.address(12, 0, 1));
+    auto stream = static_cast<wf_stream_t>(r.address(12, 0, kBytes));
     return without_gil([&] {
       return g_attn(&d, plan, table, prefix, q, k_pool, v_pool, out, lse, float(scale), workspace,
                     bytes < 0 ? 0 : size_t(bytes), stream);

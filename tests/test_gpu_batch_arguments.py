@@ -1,0 +1,66 @@
+"""Refusals of the batch calls, each from a call that is first seen to succeed
+and of which one argument is then changed: a check that was missing would let
+the changed call through (or refuse it for another reason than the one named)."""
+import pytest
+import torch
+
+from chunk_causal_attention_block_b200 import wf
+from tests.batch_common import Step
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    wf.lib()
+    yield
+
+
+class Calls:
+    """The three calls of a step, argument by argument."""
+
+    def __init__(self, **kw):
+        s = self.step = Step([20, 3, 0], [2, 30, 1], prefix=50, held=[2, 1, 0], **kw)
+        self.f = dict(tables=wf.wf_batch_tables, append=wf.wf_batch_append, attn=wf.wf_batch_attn)
+        self.args = dict(
+            tables=dict(s.d),
+            append=dict(plan=s.d["plan"], slot_map=s.d["slot_map"], k=s.k, v=s.v, k_pool=s.k_pool, v_pool=s.v_pool, q=s.q,
+                        rope=s.rope, q_rot=s.q_rot),
+            attn=dict(plan=s.d["plan"], block_table=s.d["block_table"], prefix_table=s.prefix_dev, q=s.q_rot,
+                      k_pool=s.k_pool, v_pool=s.v_pool, out=s.out, lse=s.lse, workspace=s.ws))
+
+    def __call__(self, call, **change):
+        self.f[call](self.step.desc, **{**self.args[call], "stream": self.step.stream, **change})
+
+    def good(self):
+        for call in self.f:
+            self(call)
+        return self.step
+
+    def refused(self, call, code=wf.WF_ERR_INVALID_ARG, **change):
+        with pytest.raises(wf.WfError) as e:
+            self(call, **change)
+        assert e.value.code == code, str(e.value)
+        return str(e.value)
+
+    def check(self):
+        """The step's results are those of the good calls: no refused one ran."""
+        self.step.check_tables()
+        self.step.check_attention()
+
+
+OTHERS = {torch.int32: (torch.float32, torch.uint32, torch.int64), torch.float32: (torch.int32, torch.float64),
+          torch.bfloat16: (torch.float16, torch.int16, torch.float32), torch.uint8: (torch.int16, torch.float32)}
+
+
+def test_tensors_of_other_types_are_refused():
+    c = Calls()
+    c.good()
+    for call, args in c.args.items():
+        for name, x in args.items():
+            for t in OTHERS[x.dtype]:
+                other = torch.zeros(x.shape, dtype=t, device="cuda")
+                assert f"{name} is of type" in c.refused(call, **{name: other}), (call, name, t)
+    c.check()
