@@ -12,7 +12,10 @@
 //
 // An argument is a CUDA tensor, dense, of the type and at least the size that
 // the call may touch and on the device of the plan; None; or a raw address,
-// which its owner vouches for.
+// which its owner vouches for.  A tensor of more dimensions than one also has
+// to have rows of the documented length: one with longer rows (spare table
+// columns, more heads) would hold enough elements and be read at the wrong
+// stride.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -39,6 +42,29 @@ constexpr int kAnyDevice = -1;
 constexpr auto kInt = at::ScalarType::Int, kFloat = at::ScalarType::Float, kBf16 = at::ScalarType::BFloat16;
 constexpr auto kBytes = at::ScalarType::Undefined;  // memory without a type of its own: elements of one byte
 
+// Rows that a tensor consists of: `row` elements, their last dimension `inner`
+// (or all of the row, or `flat`, several rows in one).
+struct Rows {
+  int64_t row, inner, flat;
+  explicit Rows(int64_t n) : row(n), inner(n), flat(n) {}
+  Rows(int64_t n, int64_t last) : row(n), inner(last), flat(n) {}
+  Rows(int64_t n, int64_t last, int64_t all) : row(n), inner(last), flat(all) {}
+
+  // Of n elements that the call may touch; with a single row, its end does not matter.
+  bool fit(const at::Tensor& t, int64_t n) const {
+    const auto sizes = t.sizes();
+    size_t dims = sizes.size();
+    while (dims > 1 && sizes[dims - 1] == 1) --dims;
+    if (dims < 2 || n <= row) return true;
+    const int64_t last = sizes[dims - 1];
+    if (last == flat || last == row) return true;
+    int64_t product = 1;
+    for (size_t i = dims; i-- > 0;)
+      if ((product *= sizes[i]) == row) return last == inner;
+    return false;
+  }
+};
+
 // Turns arguments into addresses.
 struct Reader {
   const char* const* names;
@@ -54,13 +80,18 @@ struct Reader {
     return p;
   }
 
-  void* address(int i, int64_t n, at::ScalarType type) const {
+  void* address(int i, int64_t n, at::ScalarType type, const Rows* rows = nullptr) const {
     PyObject* x = args[i];
     if (x == Py_None) return nullptr;
     if (const at::Tensor* t = tensor(x)) {
       if (type == kBytes ? t->itemsize() != 1 : t->scalar_type() != type)
         throw Refused{std::string(names[i]) + " is of type " + c10::toString(t->scalar_type()) + " where " +
                       (type == kBytes ? "bytes" : c10::toString(type)) + " is needed"};
+      if (rows && !rows->fit(*t, n)) {
+        std::ostringstream s;
+        s << names[i] << " is of shape " << t->sizes() << " where rows of " << rows->row << " elements are needed";
+        throw Refused{s.str()};
+      }
       const bool dense = t->layout() == at::kStrided && t->is_contiguous();
       if (dense && t->is_cuda() && t->numel() >= n && (device == kAnyDevice || t->get_device() == device))
         return t->data_ptr();
@@ -136,11 +167,13 @@ PyObject* tables(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     void* plan = r.plan(1);
     auto i32 = [&](int i, int64_t n) { return static_cast<int32_t*>(r.address(i, n, kInt)); };
     const int64_t B = d.max_requests, T = d.max_tokens;
+    const Rows columns(d.max_request_pages);
     int32_t *cached = i32(2, B), *fresh = i32(3, B), *prefix_len = i32(4, 1), *held = i32(5, B);
     const int64_t num_free = r.number(7, 6, false);
     if (num_free > INT32_MAX || num_free < INT32_MIN) throw Refused{"num_free does not fit"};
     int32_t *free_pages = i32(6, num_free), *head = i32(8, 1), *head_out = i32(9, 1), *held_out = i32(10, B);
-    int32_t *table = i32(11, B * d.max_request_pages), *start = i32(12, B + 1), *slots = i32(13, T), *pos = i32(14, T);
+    int32_t *table = static_cast<int32_t*>(r.address(11, B * d.max_request_pages, kInt, &columns)),
+            *start = i32(12, B + 1), *slots = i32(13, T), *pos = i32(14, T);
     const int64_t plan_bytes = r.number(15, 1, true);
     auto stream = static_cast<wf_stream_t>(r.address(16, 0, kBytes));
     return without_gil([&] {
@@ -158,10 +191,13 @@ PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     // a step may hold fewer tokens than max_tokens: only the device knows, so room for all is asked for
     const int64_t T = d.max_tokens, kv = int64_t(d.num_kv_heads) * d.head_dim, q_size = T * d.num_heads * d.head_dim;
     const int64_t pool = int64_t(d.pool_pages) * d.page_tokens * kv;
+    const Rows q_rows(int64_t(d.num_heads) * d.head_dim, d.head_dim), kv_rows(kv, d.head_dim),
+        pool_rows(kv, d.head_dim, d.page_tokens * kv), rope_rows(d.head_dim, 2);
     auto slots = static_cast<const int32_t*>(r.address(2, T, kInt));
-    auto rope = static_cast<const float*>(r.address(3, T * d.head_dim, kFloat));
-    void *q = r.address(4, q_size, kBf16), *k = r.address(5, T * kv, kBf16), *v = r.address(6, T * kv, kBf16);
-    void *q_rot = r.address(7, q_size, kBf16), *k_pool = r.address(8, pool, kBf16), *v_pool = r.address(9, pool, kBf16);
+    auto rope = static_cast<const float*>(r.address(3, T * d.head_dim, kFloat, &rope_rows));
+    void *q = r.address(4, q_size, kBf16, &q_rows), *q_rot = r.address(7, q_size, kBf16, &q_rows);
+    void *k = r.address(5, T * kv, kBf16, &kv_rows), *v = r.address(6, T * kv, kBf16, &kv_rows);
+    void *k_pool = r.address(8, pool, kBf16, &pool_rows), *v_pool = r.address(9, pool, kBf16, &pool_rows);
     auto stream = static_cast<wf_stream_t>(r.address(10, 0, kBytes));
     return without_gil([&] { return g_append(&d, plan, slots, rope, q, k, v, q_rot, k_pool, v_pool, stream); });
   });
@@ -174,11 +210,13 @@ PyObject* attn(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     void* plan = r.plan(1);
     const int64_t T = d.max_tokens, kv = int64_t(d.num_kv_heads) * d.head_dim, q_size = T * d.num_heads * d.head_dim;
     const int64_t pool = int64_t(d.pool_pages) * d.page_tokens * kv;
-    auto table = static_cast<const int32_t*>(r.address(2, int64_t(d.max_requests) * d.max_request_pages, kInt));
+    const Rows q_rows(int64_t(d.num_heads) * d.head_dim, d.head_dim), pool_rows(kv, d.head_dim, d.page_tokens * kv),
+        columns(d.max_request_pages), lse_rows(T);
+    auto table = static_cast<const int32_t*>(r.address(2, int64_t(d.max_requests) * d.max_request_pages, kInt, &columns));
     auto prefix = static_cast<const int32_t*>(r.address(3, d.max_prefix_pages, kInt));
-    void *q = r.address(4, q_size, kBf16), *k_pool = r.address(5, pool, kBf16), *v_pool = r.address(6, pool, kBf16);
-    void* out = r.address(7, q_size, kBf16);
-    auto lse = static_cast<float*>(r.address(8, T * d.num_heads, kFloat));
+    void *q = r.address(4, q_size, kBf16, &q_rows), *out = r.address(7, q_size, kBf16, &q_rows);
+    void *k_pool = r.address(5, pool, kBf16, &pool_rows), *v_pool = r.address(6, pool, kBf16, &pool_rows);
+    auto lse = static_cast<float*>(r.address(8, T * d.num_heads, kFloat, &lse_rows));
     const double scale = PyFloat_AsDouble(args[9]);
     if (scale == -1.0 && PyErr_Occurred()) throw Refused{"softmax_scale is not a number"};
     void* workspace = r.address(10, 0, kBytes);

@@ -4,7 +4,7 @@ Argument marshalling only: every step of the hot path runs in the library's
 CUDA kernels.  Functions keep the C names.  Tensors may be passed as torch
 tensors (their data_ptr is used) or raw integer addresses; streams as
 ``torch.cuda.Stream`` or integer handles (``None`` = legacy default stream).
-The batch calls check their tensors (device, type, layout, room) in
+The batch calls check their tensors (device, type, layout, row length, room) in
 ``_wf_torch.so`` before they pass them on; the others take any address.
 Loading fails loudly when the library has not been built: there is no
 fallback implementation.

@@ -66,3 +66,43 @@ def test_a_tensor_of_another_type_is_refused_for_its_type(call, name):
               torch.bfloat16: (torch.float16, torch.int16, torch.float32), torch.uint8: (torch.int16,)}[good.dtype]
     for t in others:
         assert f"{name} is of type" in reason(call, **{name: good.to(t)}), t
+
+
+@pytest.mark.parametrize("call,name,shape", [
+    *[(call, "block_table", s) for call in ("tables", "attn") for s in ((3, 6), (4, 4), (5, 3), (1, 3, 6))],
+    *[("attn", "lse", s) for s in ((4, 41), (5, 36), (40, 4), (2, 2, 80))],
+    *[(call, n, s) for call, n in (("append", "q"), ("append", "q_rot"), ("attn", "q"), ("attn", "out"))
+      for s in ((40, 5, 64), (40, 64, 4), (40, 320), (20, 8, 64), (4, 40, 64), (40, 2, 128), (20, 512))],
+    *[("append", n, s) for n in ("k", "v") for s in ((40, 4, 64), (40, 64, 2), (40, 1, 128 * 2), (2, 40, 64))],
+    *[(call, n, s) for call in ("append", "attn") for n in ("k_pool", "v_pool")
+      for s in ((160, 3, 64), (160, 64, 2), (2, 160, 64), (10, 2, 16, 64), (80, 256), (10, 16, 3, 64))],
+    *[("append", "rope", s) for s in ((40, 32, 3), (40, 2, 32), (40, 65), (40, 33, 2), (40, 64, 2))],
+])
+def test_rows_of_another_length_are_refused(call, name, shape):
+    good = CALLS[call][1][name]
+    assert f"{name} is of shape" in reason(call, **{name: torch.zeros(shape, dtype=good.dtype)})
+
+
+@pytest.mark.parametrize("call,name,shape", [
+    *[(call, "block_table", s) for call in ("tables", "attn") for s in ((15,), (20,), (4, 5), (1, 3, 5), (3, 5, 1))],
+    ("attn", "prefix_table", (1, 2)), ("attn", "prefix_table", (2, 1)), ("attn", "prefix_table", (7,)),
+    *[("attn", "lse", s) for s in ((160,), (5, 40), (2, 2, 40))],
+    *[(call, n, s) for call, n in (("append", "q"), ("append", "q_rot"), ("attn", "q"), ("attn", "out"))
+      for s in ((41, 4, 64), (40, 256), (40 * 256,), (40, 2, 2, 64), (2, 20, 4, 64))],
+    *[("append", n, s) for n in ("k", "v") for s in ((44, 2, 64), (40, 128), (2, 20, 2, 64), (5120,))],
+    *[(call, n, s) for call in ("append", "attn") for n in ("k_pool", "v_pool")
+      for s in ((10, 16, 2, 64), (160, 128), (10, 2048), (11, 2048), (10, 16, 128), (20480,))],
+    *[("append", "rope", s) for s in ((40, 64), (1, 40, 32, 2), (2560,))],
+])
+def test_shapes_of_the_documented_rows_are_not(call, name, shape):
+    # (what is wrong with them is where they lie)
+    good = CALLS[call][1][name]
+    assert "on cpu" in reason(call, **{name: torch.zeros(shape, dtype=good.dtype)})
+
+
+def test_the_end_of_a_single_row_does_not_matter():
+    one = wf.make_batch_desc(1, 1, 64, 16, 10, max_requests=1, max_tokens=1, max_request_pages=5, num_ctas=8)
+    for shape in ((1, 9), (2, 3), (5, 1)):
+        with pytest.raises(wf.WfError, match="on cpu"):
+            wf.wf_batch_attn(one, AT, i32(*shape), None, 2 * AT, 3 * AT, 4 * AT, 5 * AT, f32(1, 1), workspace=6 * AT,
+                             workspace_bytes=1 << 30)

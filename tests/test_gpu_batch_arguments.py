@@ -64,3 +64,24 @@ def test_tensors_of_other_types_are_refused():
                 other = torch.zeros(x.shape, dtype=t, device="cuda")
                 assert f"{name} is of type" in c.refused(call, **{name: other}), (call, name, t)
     c.check()
+
+
+def test_rows_of_another_length_are_refused():
+    c = Calls()
+    c.good()
+    cols, cap = c.step.desc.max_request_pages, c.step.desc.max_tokens
+    zeros = lambda t, *shape: torch.zeros(*shape, dtype=t, device="cuda")  # noqa: E731
+    for call, name, x in (("tables", "block_table", zeros(torch.int32, 3, cols + 1)),
+                          ("attn", "block_table", zeros(torch.int32, 3, cols + 1)),
+                          ("attn", "lse", zeros(torch.float32, 4, cap + 1)),
+                          ("attn", "q", zeros(torch.bfloat16, cap, 5, 128)),
+                          ("attn", "out", zeros(torch.bfloat16, cap, 128, 4)),
+                          ("append", "k_pool", zeros(torch.bfloat16, c.step.k_pool.shape[0], 3, 128)),
+                          ("append", "rope", zeros(torch.float32, cap, 2, 64))):
+        assert f"{name} is of shape" in c.refused(call, **{name: x}), (call, name)
+    # flattened, the same memory is taken
+    pool = lambda x: x.view(-1, c.step.page, 2, 128)  # noqa: E731
+    for call in ("append", "attn"):
+        c(call, q=c.step.q.view(cap, -1) if call == "append" else c.step.q_rot.flatten(),
+          k_pool=pool(c.step.k_pool), v_pool=pool(c.step.v_pool))
+    c.check()
