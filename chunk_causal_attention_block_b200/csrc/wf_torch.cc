@@ -106,15 +106,17 @@ struct Reader {
     return p;
   }
 
-  // A number, or what the tensor args[of] holds if it is None.
+  // A number, or what the tensor args[of] holds if it is None.  No more than that is believed.
   int64_t number(int i, int of, bool bytes) const {
+    const at::Tensor* t = tensor(args[of]);
     if (args[i] != Py_None) {
       const int64_t v = PyLong_AsLongLong(args[i]);
       if (v == -1 && PyErr_Occurred()) throw Refused{std::string(names[i]) + " is not a number"};
+      if (t && v > (bytes ? int64_t(t->nbytes()) : t->numel()))
+        throw Refused{std::string(names[i]) + " is more than " + names[of] + " holds"};
       return v;
     }
     if (args[of] == Py_None) return 0;
-    const at::Tensor* t = tensor(args[of]);
     if (!t) throw Refused{std::string(names[i]) + " is needed where " + names[of] + " is an address"};
     return bytes ? int64_t(t->nbytes()) : t->numel();
   }
@@ -164,6 +166,7 @@ PyObject* tables(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
                                       "free_head", "free_head_out", "held_out", "block_table", "token_start",
                                       "slot_map", "positions", "plan_bytes", "stream"};
   return guarded(names, args, nargs, [](const wf_batch_desc& d, Reader r) {
+    const int64_t plan_bytes = r.number(15, 1, true);
     void* plan = r.plan(1);
     auto i32 = [&](int i, int64_t n) { return static_cast<int32_t*>(r.address(i, n, kInt)); };
     const int64_t B = d.max_requests, T = d.max_tokens;
@@ -174,7 +177,6 @@ PyObject* tables(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     int32_t *free_pages = i32(6, num_free), *head = i32(8, 1), *head_out = i32(9, 1), *held_out = i32(10, B);
     int32_t *table = static_cast<int32_t*>(r.address(11, B * d.max_request_pages, kInt, &columns)),
             *start = i32(12, B + 1), *slots = i32(13, T), *pos = i32(14, T);
-    const int64_t plan_bytes = r.number(15, 1, true);
     auto stream = static_cast<wf_stream_t>(r.address(16, 0, kBytes));
     return without_gil([&] {
       return g_tables(&d, cached, fresh, prefix_len, held, free_pages, int32_t(num_free), head, head_out, held_out, table,

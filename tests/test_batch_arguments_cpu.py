@@ -106,3 +106,13 @@ def test_the_end_of_a_single_row_does_not_matter():
         with pytest.raises(wf.WfError, match="on cpu"):
             wf.wf_batch_attn(one, AT, i32(*shape), None, 2 * AT, 3 * AT, 4 * AT, 5 * AT, f32(1, 1), workspace=6 * AT,
                              workspace_bytes=1 << 30)
+
+
+def test_a_size_above_the_tensors_is_refused():
+    small = torch.zeros(100, dtype=torch.uint8)
+    for n in (101, 1 << 30):
+        assert "plan_bytes is more than plan holds" in reason("tables", plan=small, plan_bytes=n)
+        assert "num_free is more than free_pages holds" in reason("tables", free_pages=i32(100), num_free=n)
+    # not more: what is wrong is where they lie
+    assert "on cpu" in reason("tables", plan=small, plan_bytes=99)
+    assert "on cpu" in reason("tables", free_pages=i32(100), num_free=100)

@@ -85,3 +85,19 @@ def test_rows_of_another_length_are_refused():
         c(call, q=c.step.q.view(cap, -1) if call == "append" else c.step.q_rot.flatten(),
           k_pool=pool(c.step.k_pool), v_pool=pool(c.step.v_pool))
     c.check()
+
+
+def test_a_size_above_the_tensors_is_refused():
+    c = Calls()
+    c.good()
+    plan, ws = c.step.d["plan"], c.step.ws
+    c("tables", plan_bytes=plan.numel())
+    c("attn", workspace_bytes=ws.numel())
+    for n in (plan.numel() + 1, 1 << 40):
+        assert "plan_bytes is more" in c.refused("tables", plan_bytes=n)
+    for n in (ws.numel() + 1, 1 << 40):
+        assert "workspace_bytes is more" in c.refused("attn", workspace_bytes=n)
+    assert "num_free is more" in c.refused("tables", num_free=c.step.d["free_pages"].numel() + 1)
+    c.refused("tables", wf.WF_ERR_WORKSPACE, plan_bytes=plan.numel() - 257)
+    c.refused("attn", wf.WF_ERR_WORKSPACE, workspace_bytes=ws.numel() - 257)
+    c.check()
