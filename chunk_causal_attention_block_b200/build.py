@@ -72,7 +72,7 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
 
 
 def _build_torch_calls(verbose: bool):
-    newest = max(os.path.getmtime(f) for f in (TORCH_SRC, os.path.join(INCLUDE, "wf.h")))
+    newest = max(os.path.getmtime(f) for f in [TORCH_SRC] + _headers())
     if os.path.exists(TORCH_LIB) and os.path.getmtime(TORCH_LIB) >= newest:
         return
     import torch
@@ -80,7 +80,7 @@ def _build_torch_calls(verbose: bool):
     # torch's exceptions)
     root = os.path.dirname(torch.__file__)
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE, "-I", CSRC,
            "-isystem", os.path.join(root, "include"),
            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"], "-o", TORCH_LIB, TORCH_SRC,

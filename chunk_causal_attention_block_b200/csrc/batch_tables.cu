@@ -432,7 +432,7 @@ BatchLayout batch_layout(const wf_batch_desc* d) {
   L.error = WF_ERR_CAPACITY;
   // the work list's 64-bit cost arithmetic, int32 token and page indices
   const int64_t kMaxKeys = int64_t(1) << 27;
-  if (K > 256 || H > 4096 || d->max_requests > 8192 || d->max_tokens > (1 << 22) || d->num_ctas > 256 ||
+  if (K > 256 || H > 4096 || d->max_requests > 8192 || d->max_tokens > (1 << 22) || d->num_ctas > WF_BATCH_MAX_CTAS ||
       d->pool_pages * P > 0x7FFFFFFF || int64_t(d->max_requests) * d->max_request_pages > 0x7FFFFFFF ||
       d->max_request_pages * P > kMaxKeys || d->max_prefix_pages * P > kMaxKeys)
     return L;
@@ -443,7 +443,7 @@ BatchLayout batch_layout(const wf_batch_desc* d) {
       L.error = WF_ERR_CUDA;
       return L;
     }
-    L.ctas = sms < 256 ? sms : 256;
+    L.ctas = sms < WF_BATCH_MAX_CTAS ? sms : WF_BATCH_MAX_CTAS;
   }
   L.group = int32_t(H / K);
   L.tile_tokens = 128 / L.group;
@@ -454,7 +454,7 @@ BatchLayout batch_layout(const wf_batch_desc* d) {
   L.max_ctok = ctok < d->max_tokens ? ctok : d->max_tokens;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   L.off_starts = sizeof(wf_batch_hdr);
-  L.off_units = up(L.off_starts + size_t(L.ctas) * sizeof(wf_batch_start));
+  L.off_units = up(WF_BATCH_PLAN_HEAD);
   L.off_pre = up(L.off_units + size_t(L.max_units) * sizeof(wf_batch_unit));
   L.off_ctok = up(L.off_pre + size_t(L.max_units + 1) * sizeof(int64_t));
   L.off_ctok_list = up(L.off_ctok + size_t(d->max_tokens) * sizeof(int32_t));

@@ -62,6 +62,12 @@ struct wf_batch_ctok {
 };
 static_assert(sizeof(wf_batch_hdr) == 256, "batch plan header layout");
 
+// What a call reads of any plan, before it knows whether it was built for its
+// own description: the header and its CTAs' starts.  Every plan has room for
+// the most CTAs, so that another description's, however small, can be read.
+#define WF_BATCH_MAX_CTAS 256
+#define WF_BATCH_PLAN_HEAD (sizeof(wf_batch_hdr) + WF_BATCH_MAX_CTAS * sizeof(wf_batch_start))
+
 namespace wf {
 
 // Sizes and offsets that follow from a description (valid if ok).

@@ -26,7 +26,7 @@
 #include <sstream>
 #include <string>
 
-#include "wf.h"
+#include "wf_batch.h"
 
 namespace {
 
@@ -73,9 +73,10 @@ struct Reader {
 
   static const at::Tensor* tensor(PyObject* x) { return THPVariable_Check(x) ? &THPVariable_Unpack(x) : nullptr; }
 
-  // The call's plan settles the device of all its tensors.
+  // The call's plan settles the device of all its tensors.  (Kernels that read one find out by themselves whether
+  // it was built for the call's description.)
   void* plan(int i) {
-    void* p = address(i, 0, kBytes);
+    void* p = address(i, WF_BATCH_PLAN_HEAD, kBytes);
     if (const at::Tensor* t = tensor(args[i])) device = t->get_device();
     return p;
   }

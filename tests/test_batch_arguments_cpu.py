@@ -116,3 +116,15 @@ def test_a_size_above_the_tensors_is_refused():
     # not more: what is wrong is where they lie
     assert "on cpu" in reason("tables", plan=small, plan_bytes=99)
     assert "on cpu" in reason("tables", free_pages=i32(100), num_free=100)
+
+
+def test_every_plan_holds_what_is_read_of_it_before_it_is_known_to_be_the_calls():
+    # 256 bytes of header and 8 for each of the up to 256 blocks of a call
+    head = 256 + 256 * 8
+    for ctas in (1, 2, 256):
+        assert wf.wf_batch_plan_bytes(wf.make_batch_desc(1, 1, 64, 8, 1, max_requests=1, max_tokens=1,
+                                                         max_request_pages=1, num_ctas=ctas)) >= head
+    for call in ("tables", "append", "attn"):
+        short = torch.zeros(head - 1, dtype=torch.uint8)
+        extra = dict(plan_bytes=None) if call == "tables" else {}
+        assert f"where {head} are needed" in reason(call, plan=short, **extra)

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from chunk_causal_attention_block_b200 import wf
-from tests.batch_common import Step
+from tests.batch_common import SENTINEL, Step
 
 pytestmark = pytest.mark.gpu
 
@@ -101,3 +101,29 @@ def test_a_size_above_the_tensors_is_refused():
     c.refused("tables", wf.WF_ERR_WORKSPACE, plan_bytes=plan.numel() - 257)
     c.refused("attn", wf.WF_ERR_WORKSPACE, workspace_bytes=ws.numel() - 257)
     c.check()
+
+
+@pytest.mark.parametrize("change", [dict(block=2), dict(page=32), dict(H=8, Hkv=4), dict(spare_tokens=4),
+                                    dict(num_ctas=255), dict(D=64), dict(spare_cols=2), dict(smallest=True)])
+def test_a_plan_built_for_another_description_does_nothing(change):
+    # 256 blocks, more than any other plan here has shares
+    s = Step([20, 3], [2, 30], prefix=50, num_ctas=256)
+    other = Step([0], [1], H=1, Hkv=1, D=64, page=8, num_ctas=1, spare_tokens=0, spare_cols=0) \
+        if change.pop("smallest", False) else Step([20, 3], [2, 30], prefix=50, **{"num_ctas": 256, **change})
+    other.tables()
+    s.tables()  # (the slots; its own plan stays unused)
+    k, v = s.k_pool.clone(), s.v_pool.clone()
+    # the plan ends where its buffer does
+    wf.wf_batch_append(s.desc, other.d["plan"], s.d["slot_map"], s.k, s.v, s.k_pool, s.v_pool, q=s.q, rope=s.rope,
+                       q_rot=s.q_rot, stream=s.stream)
+    wf.wf_batch_attn(s.desc, other.d["plan"], s.d["block_table"], s.prefix_dev, s.q, s.k_pool, s.v_pool, s.out, s.lse,
+                     workspace=s.ws, stream=s.stream)
+    assert wf.wf_attn_workspace_status(s.ws, s.stream)[0] == wf.WF_ERR_PLAN
+    assert (s.out == SENTINEL).all() and (s.lse == SENTINEL).all() and (s.q_rot == SENTINEL).all()
+    for now, before in ((s.k_pool, k), (s.v_pool, v)):
+        assert torch.equal(now.view(torch.int16), before.view(torch.int16))
+    # nothing is left of it: the step's own plan still serves
+    wf.wf_attn_workspace_init(s.ws, s.stream)
+    s.append()
+    s.attend()
+    s.check_attention()
