@@ -114,11 +114,14 @@ extern "C" wf_status wf_batch_append(const wf_batch_desc* desc, const void* plan
   // Q only turns: without angles there is nothing to do
   if (rope ? (!q || !q_rot) : (q || q_rot)) return WF_ERR_INVALID_ARG;
   // nothing that other threads still read is written over (a Q row is turned by the threads that read it)
-  const void* in[] = {k, v, rope, slot_map, plan};
-  for (const void* i : in)
-    if (i && (i == k_pool || i == v_pool || i == q_rot)) return WF_ERR_INVALID_ARG;
-  if (k_pool == v_pool || (q && (q == k_pool || q == v_pool || q_rot == k_pool || q_rot == v_pool)))
-    return WF_ERR_INVALID_ARG;
+  constexpr size_t kBf16 = 2;
+  const size_t T = size_t(desc->max_tokens), D = size_t(desc->head_dim);
+  const size_t q_bytes = T * size_t(desc->num_heads) * D * kBf16, kv_bytes = T * size_t(desc->num_kv_heads) * D * kBf16;
+  const size_t pool_bytes = size_t(desc->pool_pages) * size_t(desc->page_tokens) * size_t(desc->num_kv_heads) * D * kBf16;
+  const wf::Span in[] = {{k, kv_bytes}, {v, kv_bytes}, {rope, T * D * sizeof(float)}, {slot_map, T * sizeof(int32_t)},
+                         {plan, L.plan_bytes}, {q != q_rot ? q : nullptr, q_bytes}};
+  const wf::Span out[] = {{q_rot, q_bytes}, {k_pool, pool_bytes}, {v_pool, pool_bytes}};
+  if (wf::written_over(out, in)) return WF_ERR_INVALID_ARG;
   if (misaligned(plan) || misaligned(rope) || misaligned(q) || misaligned(k) || misaligned(v) || misaligned(q_rot) ||
       misaligned(k_pool) || misaligned(v_pool) || reinterpret_cast<uintptr_t>(slot_map) % 4)
     return WF_ERR_ALIGNMENT;

@@ -1624,7 +1624,16 @@ extern "C" wf_status wf_batch_attn(const wf_batch_desc* desc, const void* plan, 
   if (L.error != WF_OK) return L.error;
   if (!plan || !block_table || !q || !k_pool || !v_pool || !out || !workspace) return WF_ERR_INVALID_ARG;
   if (desc->max_prefix_pages > 0 && !prefix_table) return WF_ERR_INVALID_ARG;
-  if (out == q || out == k_pool || out == v_pool) return WF_ERR_INVALID_ARG;
+  // other blocks still read what one of them would write over
+  constexpr size_t kBf16 = 2;
+  const size_t T = size_t(desc->max_tokens), H = size_t(desc->num_heads), D = size_t(desc->head_dim);
+  const size_t pool_bytes = size_t(desc->pool_pages) * size_t(desc->page_tokens) * size_t(desc->num_kv_heads) * D * kBf16;
+  const wf::Span in[] = {
+      {plan, L.plan_bytes}, {q, T * H * D * kBf16}, {k_pool, pool_bytes}, {v_pool, pool_bytes},
+      {block_table, size_t(desc->max_requests) * size_t(desc->max_request_pages) * sizeof(int32_t)},
+      {prefix_table, size_t(desc->max_prefix_pages) * sizeof(int32_t)}};
+  const wf::Span results[] = {{out, T * H * D * kBf16}, {lse, T * H * sizeof(float)}, {workspace, L.workspace_bytes}};
+  if (wf::written_over(results, in)) return WF_ERR_INVALID_ARG;
   if (wf::misaligned(plan) || wf::misaligned(q) || wf::misaligned(k_pool) || wf::misaligned(v_pool) ||
       wf::misaligned(out) || wf::misaligned(workspace) || reinterpret_cast<uintptr_t>(lse) % 4 ||
       reinterpret_cast<uintptr_t>(block_table) % 4 || reinterpret_cast<uintptr_t>(prefix_table) % 4)

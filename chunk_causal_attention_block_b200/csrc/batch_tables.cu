@@ -500,19 +500,19 @@ extern "C" wf_status wf_batch_tables(const wf_batch_desc* desc, const int32_t* c
     return WF_ERR_INVALID_ARG;
   if (desc->max_prefix_pages > 0 && !prefix_len) return WF_ERR_INVALID_ARG;
   if ((held == nullptr) != (held_out == nullptr)) return WF_ERR_INVALID_ARG;
-  // every block reads the lengths while block 0 writes: no output may be an input
-  const void* in[] = {cached, fresh, prefix_len, held, free_pages, free_head};
-  const void* out[] = {free_head_out, held_out, block_table, token_start, slot_map, positions, plan};
-  for (const void* i : in)
-    for (const void* o : out)
-      if (i && i == o) return WF_ERR_INVALID_ARG;
-  for (const void* const* o = out; o != out + 7; ++o)
-    for (const void* const* other = out; other != o; ++other)
-      if (*o && *o == *other) return WF_ERR_INVALID_ARG;
-  for (const void* x : in)
-    if (reinterpret_cast<uintptr_t>(x) % 4) return WF_ERR_ALIGNMENT;
-  for (const void* x : out)
-    if (reinterpret_cast<uintptr_t>(x) % 4) return WF_ERR_ALIGNMENT;
+  // every block reads the lengths while block 0 writes: no output may lie in an input
+  constexpr size_t kWord = sizeof(int32_t);
+  const size_t B = size_t(desc->max_requests), T = size_t(desc->max_tokens);
+  const wf::Span in[] = {{cached, B * kWord}, {fresh, B * kWord}, {prefix_len, kWord}, {held, B * kWord},
+                         {free_pages, size_t(num_free) * kWord}, {free_head, kWord}};
+  const wf::Span out[] = {{free_head_out, kWord}, {held_out, B * kWord},
+                          {block_table, B * size_t(desc->max_request_pages) * kWord}, {token_start, (B + 1) * kWord},
+                          {slot_map, T * kWord}, {positions, T * kWord}, {plan, L.plan_bytes}};
+  if (wf::written_over(out, in)) return WF_ERR_INVALID_ARG;
+  for (const wf::Span& x : in)
+    if (reinterpret_cast<uintptr_t>(x.ptr) % kWord) return WF_ERR_ALIGNMENT;
+  for (const wf::Span& x : out)
+    if (reinterpret_cast<uintptr_t>(x.ptr) % kWord) return WF_ERR_ALIGNMENT;
   if (reinterpret_cast<uintptr_t>(plan) % 16) return WF_ERR_ALIGNMENT;
   if (plan_bytes < L.plan_bytes) return WF_ERR_WORKSPACE;
   if (!wf::on_current_device(plan)) return WF_ERR_INVALID_ARG;

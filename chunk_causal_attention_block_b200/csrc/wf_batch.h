@@ -86,6 +86,31 @@ struct BatchLayout {
 
 BatchLayout batch_layout(const wf_batch_desc* d);
 
+// Memory that a call may touch (ptr NULL or no bytes: none).
+struct Span {
+  const void* ptr;
+  size_t bytes;
+};
+
+inline bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.ptr), y = reinterpret_cast<uintptr_t>(b.ptr);
+  if (!x || !y || !a.bytes || !b.bytes) return false;
+  return x <= y ? y - x < a.bytes : x - y < b.bytes;
+}
+
+// Whether an output shares memory with an input or with another output: blocks
+// of one call read and write without any order between them.
+template <size_t N, size_t M>
+inline bool written_over(const Span (&out)[N], const Span (&in)[M]) {
+  for (size_t o = 0; o < N; ++o) {
+    for (size_t i = 0; i < M; ++i)
+      if (overlap(out[o], in[i])) return true;
+    for (size_t i = 0; i < o; ++i)
+      if (overlap(out[o], out[i])) return true;
+  }
+  return false;
+}
+
 // Whether ptr is memory of the current device: elsewhere a kernel would fault on it.
 bool on_current_device(const void* ptr);
 

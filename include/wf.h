@@ -376,6 +376,9 @@ wf_status wf_chunk_causal_attn_fp8(const void* host_plan, const void* dev_plan, 
  * block_table [B, max_request_pages], row b listing b's pages in order;
  * prefix_table [max_prefix_pages] likewise.  Arrays of T entries have room for
  * max_tokens; the calls leave what lies behind the step's T tokens as it was.
+ * No output of a call may share memory, the room behind T included, with one of
+ * its inputs or with another output (WF_ERR_INVALID_ARG): blocks read while
+ * others write.  The one exception is q_rot, which may be q itself.
  *
  * Supported: bf16, D = 64 or 128, group up to 128, pages of 8, 16, 32, 64 or
  * 128 tokens.  fp32 and other D return WF_ERR_UNSUPPORTED.
@@ -424,11 +427,9 @@ size_t wf_batch_workspace_bytes(const wf_batch_desc* desc);
  *              token of each new token (-1 if its page lies outside the pool)
  *              and its position prefix_len + c_b + i.
  * plan:        device, >= wf_batch_plan_bytes(desc) bytes, 16-byte aligned.
- * No output may be one of the inputs or another output: every block reads the
- * lengths while results are written (use *_out of one step as the input of the
- * next).  The plan of this and the two calls below must be memory of the
- * current device (WF_ERR_INVALID_ARG otherwise), and all buffers of a call that
- * device's.
+ * Use *_out of one step as the input of the next.  The plan of this and the
+ * two calls below must be memory of the current device (WF_ERR_INVALID_ARG
+ * otherwise), and all buffers of a call that device's.
  *
  * Lengths that are wrong (negative, held below the cached pages:
  * WF_ERR_INVALID_ARG) or do not fit (max_tokens, block-table columns, prefix
@@ -489,8 +490,8 @@ wf_status wf_batch_append(const wf_batch_desc* desc, const void* plan, const int
  *        outside the pool read as zero keys and values.  Keys that a row may
  *        see must be finite; whatever lies in a page behind a request's (or
  *        the prefix's) last token is not used, NaN or not.
- * out:   device [T, H, D] (written; not q, which other blocks still read); lse:
- *        device fp32 [H, max_tokens] (the first T of each row written), or NULL.
+ * out:   device [T, H, D] (written).
+ * lse:   device fp32 [H, max_tokens] (the first T of each row written), or NULL.
  * softmax_scale: 0 means 1/sqrt(D).
  * workspace: >= wf_batch_workspace_bytes(desc) bytes, its first 256 zeroed once
  *        (wf_attn_workspace_init); it holds rows that are still to be merged, so

@@ -2,9 +2,13 @@
 refusal names the argument and what is wrong with it, so that one check cannot
 stand in for another.  The plan is a raw address here (a tensor would have to
 be on a GPU), and nothing is ever launched: all memory is the host's."""
+import os
+import subprocess
+
 import pytest
 import torch
 
+from chunk_causal_attention_block_b200 import build as wfbuild
 from chunk_causal_attention_block_b200 import wf
 
 D = dict(H=4, Hkv=2, D=64, page_tokens=16, pool_pages=10, max_requests=3, max_tokens=40, max_request_pages=5,
@@ -128,3 +132,10 @@ def test_every_plan_holds_what_is_read_of_it_before_it_is_known_to_be_the_calls(
         short = torch.zeros(head - 1, dtype=torch.uint8)
         extra = dict(plan_bytes=None) if call == "tables" else {}
         assert f"where {head} are needed" in reason(call, plan=short, **extra)
+
+
+def test_what_counts_as_shared_memory(tmp_path):
+    exe = str(tmp_path / "overlap")
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I", wfbuild.INCLUDE, "-I", wfbuild.CSRC,
+                    os.path.join(os.path.dirname(__file__), "c", "overlap.cpp"), "-o", exe], check=True)
+    assert subprocess.run([exe], capture_output=True, text=True, check=True).stdout == "0 wrong\n"

@@ -110,10 +110,12 @@ def test_a_plan_built_for_another_description_does_nothing(change):
     s = Step([20, 3], [2, 30], prefix=50, num_ctas=256)
     other = Step([0], [1], H=1, Hkv=1, D=64, page=8, num_ctas=1, spare_tokens=0, spare_cols=0) \
         if change.pop("smallest", False) else Step([20, 3], [2, 30], prefix=50, **{"num_ctas": 256, **change})
+    # (in a buffer of its own, so that the room of a plan of the call's description meets none of its results)
+    buffer = torch.zeros(other.d["plan"].numel() + s.d["plan"].numel(), dtype=torch.uint8, device="cuda")
+    other.d["plan"] = buffer[:other.d["plan"].numel()]
     other.tables()
     s.tables()  # (the slots; its own plan stays unused)
     k, v = s.k_pool.clone(), s.v_pool.clone()
-    # the plan ends where its buffer does
     wf.wf_batch_append(s.desc, other.d["plan"], s.d["slot_map"], s.k, s.v, s.k_pool, s.v_pool, q=s.q, rope=s.rope,
                        q_rot=s.q_rot, stream=s.stream)
     wf.wf_batch_attn(s.desc, other.d["plan"], s.d["block_table"], s.prefix_dev, s.q, s.k_pool, s.v_pool, s.out, s.lse,
@@ -126,4 +128,52 @@ def test_a_plan_built_for_another_description_does_nothing(change):
     wf.wf_attn_workspace_init(s.ws, s.stream)
     s.append()
     s.attend()
+    s.check_attention()
+
+
+INPUTS = dict(tables=("cached", "fresh", "prefix_len", "held", "free_pages", "free_head"),
+              append=("plan", "slot_map", "rope", "q", "k", "v"),
+              attn=("plan", "block_table", "prefix_table", "q", "k_pool", "v_pool"))
+OUTPUTS = dict(tables=("free_head_out", "held_out", "block_table", "token_start", "slot_map", "positions", "plan"),
+               append=("q_rot", "k_pool", "v_pool"), attn=("out", "lse", "workspace"))
+
+
+@pytest.mark.parametrize("call", ["tables", "append", "attn"])
+def test_results_that_share_memory_are_refused(call):
+    c = Calls()
+    c.good()
+    args = c.args[call]
+    nbytes = {name: x.numel() * x.element_size() for name, x in args.items()}
+    why = f"wf_batch_{call}: {wf.status_string(wf.WF_ERR_INVALID_ARG)}"  # the library's own, not the binding's
+    for o in OUTPUTS[call]:
+        for i in INPUTS[call] + OUTPUTS[call][:OUTPUTS[call].index(o)]:
+            # b begins where a does, or in a's last 16 (or 4) bytes
+            for a, b in ((o, i), (i, o)):
+                for at in (0, nbytes[a] - (16 if nbytes[a] % 16 == 0 else 4)):
+                    if at == 0 and {a, b} == {"q", "q_rot"}:
+                        continue  # in place
+                    raw = torch.zeros(nbytes[a] + nbytes[b], dtype=torch.uint8, device="cuda")
+                    views = {a: raw[:nbytes[a]], b: raw[at:at + nbytes[b]]}
+                    views = {n: x.view(args[n].dtype).view(args[n].shape) for n, x in views.items()}
+                    assert c.refused(call, **views) == why, (a, b, at)
+    c.check()
+
+
+def test_buffers_right_behind_one_another_are_taken():
+    c = Calls()
+    s = c.step
+    tensors = [(s.d, n) for n in s.d] + [(s.__dict__, n) for n in ("k_pool", "v_pool", "q", "k", "v", "rope", "q_rot", "out",
+                                                                   "lse", "ws", "prefix_dev")]
+    sizes = [-(-where[n].numel() * where[n].element_size() // 16) * 16 for where, n in tensors]
+    arena = torch.zeros(sum(sizes), dtype=torch.uint8, device="cuda")
+    for (where, n), size in zip(tensors, sizes):
+        x, (part, arena) = where[n], arena.split([size, arena.numel() - size])
+        where[n] = part[:x.numel() * x.element_size()].view(x.dtype).view(x.shape)
+        where[n].copy_(x)
+    k, v = s.k_pool.clone(), s.v_pool.clone()
+    s.tables()
+    s.append()
+    s.attend()
+    s.check_tables()
+    s.check_append(k, v)
     s.check_attention()
