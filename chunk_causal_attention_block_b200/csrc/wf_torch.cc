@@ -11,7 +11,8 @@
 // us.)
 //
 // An argument is a CUDA tensor, dense, of the type and at least the size that
-// the call may touch and on the device of the plan; None; or a raw address,
+// the call may touch and on the device of the plan (the current one, if the plan
+// is an address: the library looks where that lies); None; or a raw address,
 // which its owner vouches for.  A tensor of more dimensions than one also has
 // to have rows of the documented length: one with longer rows (spare table
 // columns, more heads) would hold enough elements and be read at the wrong
@@ -19,6 +20,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -38,7 +40,7 @@ struct Refused {
   std::string why;
 };
 
-constexpr int kAnyDevice = -1;
+constexpr int kAnyDevice = -1, kCurrentDevice = -2;
 constexpr auto kInt = at::ScalarType::Int, kFloat = at::ScalarType::Float, kBf16 = at::ScalarType::BFloat16;
 constexpr auto kBytes = at::ScalarType::Undefined;  // memory without a type of its own: elements of one byte
 
@@ -77,8 +79,16 @@ struct Reader {
   // it was built for the call's description.)
   void* plan(int i) {
     void* p = address(i, WF_BATCH_PLAN_HEAD, kBytes);
-    if (const at::Tensor* t = tensor(args[i])) device = t->get_device();
+    const at::Tensor* t = tensor(args[i]);
+    device = t ? t->get_device() : kCurrentDevice;
     return p;
+  }
+
+  bool here(const at::Tensor& t) const {
+    if (!t.is_cuda() || device == kAnyDevice) return t.is_cuda();
+    return t.get_device() == (device == kCurrentDevice
+                                  ? c10::impl::VirtualGuardImpl(c10::DeviceType::CUDA).getDevice().index()
+                                  : device);
   }
 
   void* address(int i, int64_t n, at::ScalarType type, const Rows* rows = nullptr) const {
@@ -94,11 +104,12 @@ struct Reader {
         throw Refused{s.str()};
       }
       const bool dense = t->layout() == at::kStrided && t->is_contiguous();
-      if (dense && t->is_cuda() && t->numel() >= n && (device == kAnyDevice || t->get_device() == device))
-        return t->data_ptr();
+      if (dense && t->numel() >= n && here(*t)) return t->data_ptr();
       std::ostringstream s;
       s << names[i] << " has " << t->numel() << " elements on " << t->device() << (dense ? "" : ", not dense")
-        << " where " << n << " are needed on " << (device == kAnyDevice ? "a GPU" : "the plan's GPU");
+        << " where " << n << " are needed on " << (device == kAnyDevice       ? "a GPU"
+                                                   : device == kCurrentDevice ? "the current GPU"
+                                                                              : "the plan's GPU");
       throw Refused{s.str()};
     }
     if (!PyLong_Check(x)) throw Refused{std::string(names[i]) + " is neither a tensor nor an address nor None"};

@@ -139,3 +139,9 @@ def test_what_counts_as_shared_memory(tmp_path):
     subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I", wfbuild.INCLUDE, "-I", wfbuild.CSRC,
                     os.path.join(os.path.dirname(__file__), "c", "overlap.cpp"), "-o", exe], check=True)
     assert subprocess.run([exe], capture_output=True, text=True, check=True).stdout == "0 wrong\n"
+
+
+@pytest.mark.parametrize("call,name", EVERY)
+def test_tensors_beside_a_plan_by_address_have_to_be_on_the_current_device(call, name):
+    # (an address says nothing of the device that the other tensors have to be on)
+    assert "on the current GPU" in reason(call, **{name: CALLS[call][1][name]})

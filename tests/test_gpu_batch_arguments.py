@@ -177,3 +177,21 @@ def test_buffers_right_behind_one_another_are_taken():
     s.check_tables()
     s.check_append(k, v)
     s.check_attention()
+
+
+def test_a_plan_may_be_an_address_beside_tensors():
+    c = Calls()
+    plan = c.step.d["plan"]
+    c("tables", plan=plan.data_ptr(), plan_bytes=plan.numel())
+    c("append", plan=plan.data_ptr())
+    c("attn", plan=plan.data_ptr())
+    c.check()
+    for call, name in (("tables", "fresh"), ("append", "k"), ("attn", "out")):
+        extra = dict(plan_bytes=plan.numel()) if call == "tables" else {}
+        assert "on the current GPU" in c.refused(call, plan=plan.data_ptr(), **{name: c.args[call][name].cpu()}, **extra)
+    if torch.cuda.device_count() > 1:
+        with torch.cuda.device(1):
+            for call in c.args:
+                extra = dict(plan_bytes=plan.numel()) if call == "tables" else {}
+                assert "on the current GPU" in c.refused(call, plan=plan.data_ptr(), **extra)
+    c.check()
