@@ -59,6 +59,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <cstdlib>
+#include <mutex>
 
 #include "sm100_ptx.cuh"
 #include "wf_batch.h"
@@ -1571,6 +1572,15 @@ bool make_pool_map(CUtensorMap* tm, const void* base, int64_t tokens, int32_t he
   return encode_map(tm, base, 5, dims, strides, box);
 }
 
+// Held while a call's two kernels are launched, so that they stand right behind
+// one another: on a stream and workspace that two threads use, another call's
+// parts would otherwise come between these and their merging.  One of several
+// locks by workspace, for calls that share nothing to seldom meet (about 20 ns).
+std::mutex& between_kernels(const void* workspace) {
+  static std::mutex locks[64];
+  return locks[(reinterpret_cast<uintptr_t>(workspace) >> 8) % 64];
+}
+
 template <int D>
 wf_status launch(const wf_batch_desc* d, const BatchLayout& L, const Params& p, const void* q, const void* k_pool,
                  const void* v_pool, cudaStream_t stream) {
@@ -1594,6 +1604,7 @@ wf_status launch(const wf_batch_desc* d, const BatchLayout& L, const Params& p, 
       !make_pool_map(&tk, k_pool, pool, d->num_kv_heads, D, d->page_tokens) ||
       !make_pool_map(&tv, v_pool, pool, d->num_kv_heads, D, d->page_tokens))
     return WF_ERR_CUDA;
+  const std::lock_guard<std::mutex> both(between_kernels(p.status));
   const wf_status launched =
       launch_early(batch_attn_kernel<D>, unsigned(L.ctas), kThreads, Cfg<D>::kSmemBytes, stream, tq, tn, tk, tv, p);
   if (launched != WF_OK) return launched;

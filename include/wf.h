@@ -495,10 +495,11 @@ wf_status wf_batch_append(const wf_batch_desc* desc, const void* plan, const int
  * softmax_scale: 0 means 1/sqrt(D).
  * workspace: >= wf_batch_workspace_bytes(desc) bytes, its first 256 zeroed once
  *        (wf_attn_workspace_init); it holds rows that are still to be merged, so
- *        calls that may overlap on the GPU need one each.  Device errors are
- *        read with wf_attn_workspace_status: WF_ERR_DEVICE_TIMEOUT, or
- *        WF_ERR_PLAN if the plan was not built for this description (nothing
- *        is written then).
+ *        calls that may overlap on the GPU need one each (calls on one stream
+ *        do not, from whichever threads they come).  Device errors are read
+ *        with wf_attn_workspace_status: WF_ERR_DEVICE_TIMEOUT, or WF_ERR_PLAN
+ *        if the plan was not built for this description (nothing is written
+ *        then).
  * The result does not depend on timing: parts are merged in a fixed order.
  * Errors: WF_ERR_INVALID_ARG, WF_ERR_UNSUPPORTED, WF_ERR_CAPACITY,
  *         WF_ERR_ALIGNMENT, WF_ERR_WORKSPACE, WF_ERR_CUDA.
