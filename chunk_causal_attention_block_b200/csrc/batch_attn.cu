@@ -251,6 +251,38 @@ __device__ __forceinline__ bool warp_wait(const Shared<D>& sh, const Params& p, 
   return __all_sync(0xffffffffu, wait_bar(sh, p, bar, parity, where));
 }
 
+// The scheduler's wait for a slot of the item ring.  It lasts as long as the
+// oldest item runs (a million key tiles take 1 s), so it gives up only when no
+// K tile has been asked for within the limit: a role that is stuck expires by
+// itself and ends this wait too.
+template <int D>
+__device__ __forceinline__ bool wait_slot(const Shared<D>& sh, const Params& p, int it, int where) {
+  using C = Cfg<D>;
+  const uint32_t addr = sh.bar(C::kItemEmpty + it % kItems), parity = ((it / kItems) & 1) ^ 1;
+  if (__all_sync(0xffffffffu, mbar_try_wait(addr, parity))) return true;
+  const int lane = threadIdx.x & 31;
+  uint32_t seen = 0;
+  uint64_t since = global_timer_ns();
+#pragma unroll 1
+  while (!__all_sync(0xffffffffu, mbar_try_wait(addr, parity))) {
+    if (__any_sync(0xffffffffu, sh.aborting())) return false;
+    const uint32_t fill = lane < C::kStages ? ld_shared_u32(sh.fills(0, lane)) : 0;
+    const uint64_t now = global_timer_ns();
+    if (__any_sync(0xffffffffu, fill != seen)) {
+      seen = fill;
+      since = now;
+    } else if (__any_sync(0xffffffffu, now - since > p.timeout_ns)) {
+      if (lane == 0) {
+        st_shared_u32(sh.base + Shared<D>::kAbortAt, 1);
+        *reinterpret_cast<int4*>(p.status) =
+            make_int4(WF_ERR_DEVICE_TIMEOUT, where, int32_t(blockIdx.x), int32_t(threadIdx.x));
+      }
+      return false;
+    }
+  }
+  return true;
+}
+
 // ---------------------------------------------------------------- shares of the line of costs
 // Equal shares of `size` (the last one shorter).
 struct Line {
@@ -434,7 +466,7 @@ __device__ __forceinline__ void scheduler(const Shared<D>& sh, const Params& p, 
       todo &= todo - 1;
       const int32_t n = __shfl_sync(0xffffffffu, j1 - j0, src);
       const bool pair = __shfl_sync(0xffffffffu, r.ntok, src) > p.tile_tokens;
-      if (!warp_wait(sh, p, Cfg<D>::kItemEmpty + it % kItems, ((it / kItems) & 1) ^ 1, 40)) return;
+      if (!wait_slot<D>(sh, p, it, 40)) return;
       if (lane == src) {
         Item y;
         y.j0 = j0;
@@ -480,7 +512,7 @@ __device__ __forceinline__ void scheduler(const Shared<D>& sh, const Params& p, 
     }
     if (more) have = load_unit(p, x, head, u + lane, r, s);
   }
-  if (!warp_wait(sh, p, Cfg<D>::kItemEmpty + it % kItems, ((it / kItems) & 1) ^ 1, 41)) return;
+  if (!wait_slot<D>(sh, p, it, 41)) return;
   if (lane == 0) {
     put_item<D>(sh, it, Item{});
     mbar_arrive(sh.bar(Cfg<D>::kItemFull + it % kItems));

@@ -61,3 +61,26 @@ def test_two_threads_on_one_stream_and_workspace(kw):
 def attend(s, q, out, lse):
     wf.wf_batch_attn(s.desc, s.d["plan"], s.d["block_table"], s.prefix_dev, q, s.k_pool, s.v_pool, out, lse,
                      workspace=s.ws, stream=s.stream)
+
+
+def test_an_item_may_run_longer_than_the_wait_limit(monkeypatch):
+    # ten units of 256 rows on one block, each some 15 ms long: a slot of the block's eight items comes free only
+    # when the oldest is done, and what waits for it may not take that for a stall
+    s = Step([0], [2560], prefix=1 << 21, H=1, Hkv=1, D=64, page=128, num_ctas=1, poison=0.0)
+    s.run()
+    assert wf.wf_attn_workspace_status(s.ws, s.stream)[0] == wf.WF_OK
+    out, lse = s.out.clone(), s.lse.clone()
+    assert not (out[:s.T] == SENTINEL).any()
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    s.attend()
+    end.record()
+    end.synchronize()
+    assert start.elapsed_time(end) > 10 * 6.0  # each unit well above the limit set below
+    s.out.fill_(SENTINEL)
+    monkeypatch.setenv("WF_WAIT_TIMEOUT_MS", "3")
+    s.attend()
+    monkeypatch.delenv("WF_WAIT_TIMEOUT_MS")
+    code, detail = wf.wf_attn_workspace_status(s.ws, s.stream)
+    assert code == wf.WF_OK, detail
+    assert torch.equal(s.out, out) and torch.equal(s.lse, lse)
