@@ -487,9 +487,13 @@ wf_status wf_batch_append(const wf_batch_desc* desc, const void* plan, const int
  *
  * block_table, prefix_table (NULL if max_prefix_pages is 0): pages of the keys;
  *        the step's own K/V must be in the pool (wf_batch_append).  Entries
- *        outside the pool read as zero keys and values.  Keys that a row may
- *        see must be finite; whatever lies in a page behind a request's (or
- *        the prefix's) last token is not used, NaN or not.
+ *        outside the pool read as zero keys and values.  Whatever lies in a
+ *        page behind a request's (or the prefix's) last token is not used, NaN
+ *        or not.  The prefix and all c_b + f_b own keys of a request should be
+ *        finite: a key hidden by the mask has no part in a row's scores, but it
+ *        weighs 0 in the row's sum of values, and 0 times a value that is NaN
+ *        or infinite makes that column of O NaN.  Own keys reach no other
+ *        request's rows.
  * out:   device [T, H, D] (written).
  * lse:   device fp32 [H, max_tokens] (the first T of each row written), or NULL.
  * softmax_scale: 0 means 1/sqrt(D).
