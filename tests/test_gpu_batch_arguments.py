@@ -195,3 +195,86 @@ def test_a_plan_may_be_an_address_beside_tensors():
                 extra = dict(plan_bytes=plan.numel()) if call == "tables" else {}
                 assert "on the current GPU" in c.refused(call, plan=plan.data_ptr(), **extra)
     c.check()
+
+
+# ---------------------------------------------------------------- the library's own refusals
+def own(call, code):
+    return f"wf_batch_{call}: {wf.status_string(code)}"
+
+
+NEEDED = dict(tables=("cached", "fresh", "prefix_len", "free_pages", "free_head", "free_head_out", "block_table",
+                      "token_start", "slot_map", "positions", "plan"),
+              append=("plan", "slot_map", "k", "v", "k_pool", "v_pool", "q", "rope", "q_rot"),
+              attn=("plan", "block_table", "prefix_table", "q", "k_pool", "v_pool", "out", "workspace"))
+
+
+@pytest.mark.parametrize("call,change", [
+    *[(call, {name: None}) for call, names in NEEDED.items() for name in names],
+    ("tables", dict(held=None)), ("tables", dict(held_out=None)), ("tables", dict(num_free=-1)),
+    ("append", dict(rope=None, q_rot=None)), ("append", dict(rope=None, q=None)),
+    ("append", dict(q=None, q_rot=None)),
+    *[("attn", dict(softmax_scale=x)) for x in (-1.0, -0.5, float("nan"), float("inf"), float("-inf"))],
+])
+def test_the_library_refuses(call, change):
+    c = Calls()
+    c.good()
+    extra = {}
+    if change.get("free_pages", 0) is None:
+        extra["num_free"] = c.step.d["free_pages"].numel()
+    if call == "tables" and change.get("plan", 0) is None:
+        extra["plan_bytes"] = c.step.d["plan"].numel()
+    if change.get("workspace", 0) is None:
+        extra["workspace_bytes"] = c.step.ws.numel()
+    # (a number for the missing buffer is not what is refused: with the buffer the call goes through)
+    c(call, **extra)
+    assert c.refused(call, **change, **extra) == own(call, wf.WF_ERR_INVALID_ARG)
+    c.check()
+
+
+def test_what_may_be_left_out():
+    c = Calls()
+    c.good()
+    c("attn", lse=None)
+    c("tables", held=None, held_out=None)
+    s = Step([20, 3], [2, 30], rope=False)  # no prefix, no angles
+    s.d["prefix_len"] = None
+    s.run()
+    s.check_attention()
+
+
+@pytest.mark.parametrize("call,name", [(call, n) for call, names in dict(
+    tables=("plan",), append=("plan", "k", "v", "k_pool", "v_pool", "q", "rope", "q_rot"),
+    attn=("plan", "q", "k_pool", "v_pool", "out", "workspace")).items() for n in names])
+def test_buffers_off_their_boundary_are_refused(call, name):
+    c = Calls()
+    c.good()
+    x = c.args[call][name]
+    n = x.numel() * x.element_size()
+    raw = torch.zeros(n + 64, dtype=torch.uint8, device="cuda")
+    at = lambda by: raw[by:by + n].view(x.dtype).view(x.shape)  # noqa: E731
+    at(16).copy_(x)
+    if name not in ("q_rot", "out"):  # (on its boundary it is taken)
+        c(call, **{name: at(16)})
+    for by in (4, 8, 24):
+        assert c.refused(call, wf.WF_ERR_ALIGNMENT, **{name: at(by)}) == own(call, wf.WF_ERR_ALIGNMENT)
+    c.check()
+
+
+@pytest.mark.parametrize("call,name", [("tables", n) for n in INPUTS["tables"] + OUTPUTS["tables"][:-1]] +
+                         [("append", "slot_map"), ("attn", "block_table"), ("attn", "prefix_table"), ("attn", "lse")])
+def test_addresses_off_a_word_are_refused(call, name):
+    # (no tensor of 4-byte elements lies so: addresses)
+    c = Calls()
+    c.good()
+    args = {n: x.data_ptr() for n, x in c.args[call].items()}
+    if call == "tables":
+        args.update(num_free=c.step.d["free_pages"].numel(), plan_bytes=c.step.d["plan"].numel())
+    if call == "attn":
+        args["workspace_bytes"] = c.step.ws.numel()
+    c(call, **args)
+    # into the middle of a buffer of its own, as long twice
+    raw = torch.zeros(2 * c.args[call][name].numel() * 4 + 64, dtype=torch.uint8, device="cuda")
+    for by in (1, 2, 3):
+        assert c.refused(call, wf.WF_ERR_ALIGNMENT, **{**args, name: raw.data_ptr() + 16 + by}) == \
+            own(call, wf.WF_ERR_ALIGNMENT)
+    c.check()
