@@ -278,3 +278,40 @@ def test_addresses_off_a_word_are_refused(call, name):
         assert c.refused(call, wf.WF_ERR_ALIGNMENT, **{**args, name: raw.data_ptr() + 16 + by}) == \
             own(call, wf.WF_ERR_ALIGNMENT)
     c.check()
+
+
+# ---------------------------------------------------------------- room and layout
+@pytest.mark.parametrize("call", ["tables", "append", "attn"])
+def test_tensors_too_small_or_strided_are_refused(call):
+    c = Calls()
+    c.good()
+    for name, x in c.args[call].items():
+        short = x.flatten()[:x.numel() - 1].clone()
+        wide = torch.zeros(2 * x.numel(), dtype=x.dtype, device="cuda")[::2]
+        if name in ("plan", "workspace"):
+            # (their sizes are the library's to judge; of a plan that is only read, what every plan holds is asked for)
+            if call == "tables" or name == "workspace":
+                assert c.refused(call, wf.WF_ERR_WORKSPACE, **{name: short}) == own(call, wf.WF_ERR_WORKSPACE)
+            if name == "plan":
+                assert "2304 are needed" in c.refused(call, plan=x[:2303])
+        elif name == "free_pages":
+            assert "num_free is more" in c.refused(call, free_pages=short, num_free=x.numel())
+        else:
+            why = c.refused(call, **{name: short})
+            assert f"{name} has {x.numel() - 1} elements" in why and f"{x.numel()} are needed" in why, why
+        if x.numel() > 1:
+            assert f"{name} has {x.numel()} elements on cuda:0, not dense" in c.refused(call, **{name: wide})
+    c.check()
+
+
+@pytest.mark.parametrize("call", ["tables", "append", "attn"])
+def test_host_tensors_are_refused(call):
+    c = Calls()
+    c.good()
+    for name, x in c.args[call].items():
+        for host in (x.cpu(), x.cpu().pin_memory()):
+            assert f"{name} has {x.numel()} elements on cpu" in c.refused(call, **{name: host}), name
+    pinned = c.step.d["plan"].cpu().pin_memory()
+    extra = dict(plan_bytes=pinned.numel()) if call == "tables" else {}
+    assert c.refused(call, plan=pinned.data_ptr(), **extra) == own(call, wf.WF_ERR_INVALID_ARG)
+    c.check()
