@@ -84,3 +84,65 @@ def test_an_item_may_run_longer_than_the_wait_limit(monkeypatch):
     code, detail = wf.wf_attn_workspace_status(s.ws, s.stream)
     assert code == wf.WF_OK, detail
     assert torch.equal(s.out, out) and torch.equal(s.lse, lse)
+
+
+@pytest.mark.parametrize("before", ["nothing", "a copy", "a fill"])
+@pytest.mark.parametrize("call", ["tables", "append", "attend"])
+def test_a_call_is_the_first_of_a_graph(call, before):
+    # alone, or right behind a copy of one of its inputs (which holds something else till then) or a fill of a result
+    s = Step([200, 3, 40], [1, 9, 130], prefix=500)
+    start = dict(k=s.k_pool.clone(), v=s.v_pool.clone(), table=s.d["block_table"].clone())
+    s.run()
+    s.check_attention()
+    want = dict(out=s.out[:s.T].clone(), lse=s.lse[:, :s.T].clone(), q_rot=s.q_rot[:s.T].clone(),
+                k=s.k_pool.clone(), v=s.v_pool.clone())
+    given = dict(tables=s.d["fresh"], append=s.k, attend=s.q_rot)[call]
+    result = dict(tables=s.d["slot_map"], append=s.q_rot, attend=s.out)[call]
+    host, fill = given.cpu().pin_memory(), -9 if call == "tables" else SENTINEL
+    side = torch.cuda.Stream()
+    s.stream = side
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        if before == "a copy":
+            given.copy_(host, non_blocking=True)
+        elif before == "a fill":
+            result.fill_(fill)
+        getattr(s, call)()
+    for _ in range(3):
+        # nothing of an earlier run is left for the graph to agree with
+        if call == "tables":
+            s.d["block_table"].copy_(start["table"])
+            for name in ("token_start", "free_head_out"):
+                s.d[name].fill_(-1)
+            for name in ("slot_map", "positions"):
+                s.d[name].fill_(-9)
+            s.d["plan"].zero_()
+        elif call == "append":
+            s.k_pool.copy_(start["k"])
+            s.v_pool.copy_(start["v"])
+            s.q_rot.fill_(SENTINEL)
+        else:
+            s.out.fill_(SENTINEL)
+            s.lse.fill_(SENTINEL)
+        if before == "a copy":
+            given.fill_(0)
+        elif before == "a fill":
+            result.fill_(1)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        if call == "tables":
+            s.check_tables()
+            s.stream = torch.cuda.current_stream()
+            s.append()
+            s.attend()
+            s.stream = side
+            torch.cuda.synchronize()
+        elif call == "append":
+            assert torch.equal(s.q_rot[:s.T], want["q_rot"])
+            for name in ("k", "v"):
+                assert torch.equal(getattr(s, name + "_pool").view(torch.int16), want[name].view(torch.int16))
+            continue
+        assert torch.equal(s.out[:s.T], want["out"]) and torch.equal(s.lse[:, :s.T], want["lse"])
+        assert (s.out[s.T:] == SENTINEL).all()
