@@ -1,9 +1,12 @@
-"""Build libwf.so in-tree with nvcc for sm_100a, and _wf_torch.so, which checks
-torch tensors for the batch calls, with the host compiler.
+"""Build libwf.so in-tree with nvcc for sm_100a, and _wf_torch.<versions>.so,
+which checks torch tensors for the batch calls, with the host compiler.
 
-    python -m chunk_causal_attention_block_b200.build [--verbose]
+    python -m chunk_causal_attention_block_b200.build [--verbose] [--no-torch]
 
-Objects go to ``_build/`` (git-ignored) and are rebuilt when a source or
+A C program needs libwf.so alone: the other is left out with --no-torch, and
+where there is no torch or no g++.  It reads the fields of torch's tensors
+inline, so its name carries the torch and the Python that it was built for, and
+one for others is neither loaded nor taken for up to date.  Objects go to ``_build/`` (git-ignored) and are rebuilt when a source or
 header is newer; the shared library lands next to this file so that it
 travels with the source tree.
 """
@@ -23,7 +26,6 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libwf.so")
 TORCH_SRC = os.path.join(CSRC, "wf_torch.cc")
-TORCH_LIB = os.path.join(PKG, "_wf_torch.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
@@ -46,7 +48,14 @@ def _headers():
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
-def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
+def torch_lib() -> str:
+    """Path of the batch calls' tensor checks for the torch and the Python that run."""
+    import torch
+    version = torch.__version__.replace("+", "-")
+    return os.path.join(PKG, f"_wf_torch.torch-{version}.{sysconfig.get_config_var('SOABI')}.so")
+
+
+def build(verbose: bool = False, ptxas_verbose: bool = False, torch_calls: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     hdr_mtime = max(os.path.getmtime(h) for h in _headers())
     objs = []
@@ -67,15 +76,24 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
-    _build_torch_calls(verbose)
+    if torch_calls:
+        _build_torch_calls(verbose)
     return LIB
 
 
 def _build_torch_calls(verbose: bool):
-    newest = max(os.path.getmtime(f) for f in [TORCH_SRC] + _headers())
-    if os.path.exists(TORCH_LIB) and os.path.getmtime(TORCH_LIB) >= newest:
+    try:
+        import torch
+    except ImportError:
+        print("no torch: the batch calls' tensor checks are not built", file=sys.stderr)
         return
-    import torch
+    if not shutil.which("g++"):
+        print("no g++: the batch calls' tensor checks are not built", file=sys.stderr)
+        return
+    lib = torch_lib()
+    newest = max(os.path.getmtime(f) for f in [TORCH_SRC, os.path.abspath(__file__)] + _headers())  # (flags: this file)
+    if os.path.exists(lib) and os.path.getmtime(lib) >= newest:
+        return
     # (the g++ on the path, whose C++ runtime torch shares; one that links the runtime statically cannot catch
     # torch's exceptions)
     root = os.path.dirname(torch.__file__)
@@ -83,7 +101,7 @@ def _build_torch_calls(verbose: bool):
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE, "-I", CSRC,
            "-isystem", os.path.join(root, "include"),
            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
-           "-isystem", sysconfig.get_paths()["include"], "-o", TORCH_LIB, TORCH_SRC,
+           "-isystem", sysconfig.get_paths()["include"], "-o", lib, TORCH_SRC,
            "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -91,4 +109,5 @@ def _build_torch_calls(verbose: bool):
 
 
 if __name__ == "__main__":
-    print(build(verbose="--verbose" in sys.argv, ptxas_verbose="--ptxas" in sys.argv))
+    print(build(verbose="--verbose" in sys.argv, ptxas_verbose="--ptxas" in sys.argv,
+                torch_calls="--no-torch" not in sys.argv))

@@ -5,13 +5,14 @@ CUDA kernels.  Functions keep the C names.  Tensors may be passed as torch
 tensors (their data_ptr is used) or raw integer addresses; streams as
 ``torch.cuda.Stream`` or integer handles (``None`` = legacy default stream).
 The batch calls check their tensors (device, type, layout, row length, room) in
-``_wf_torch.so`` before they pass them on; the others take any address.
+``_wf_torch.<versions>.so`` before they pass them on; the others take any address.
 Loading fails loudly when the library has not been built: there is no
 fallback implementation.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import struct
 from typing import Optional, Sequence
@@ -276,12 +277,14 @@ def _batch_calls():
     """The batch calls' native argument checks (csrc/wf_torch.cc), bound to the loaded library."""
     global _torch_calls
     if _torch_calls is None:
-        import torch  # noqa: F401  (its libraries have to be loaded first)
-        try:
-            from . import _wf_torch as m
-        except ImportError as e:
-            raise RuntimeError("_wf_torch.so is not built (or for another torch); run "
-                               "`python -m chunk_causal_attention_block_b200.build`") from e
+        from .build import torch_lib
+        path = torch_lib()  # (imports torch, whose libraries have to be loaded first)
+        if not os.path.exists(path):
+            raise RuntimeError(f"the batch calls' tensor checks are not built for this torch and Python ({path}); run "
+                               "`python -m chunk_causal_attention_block_b200.build`")
+        spec = importlib.util.spec_from_file_location(__package__ + "._wf_torch", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
         m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                  for f in (lib().wf_batch_tables, lib().wf_batch_append, lib().wf_batch_attn)))
         _torch_calls = m
