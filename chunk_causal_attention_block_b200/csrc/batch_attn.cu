@@ -259,10 +259,9 @@ template <int D>
 __device__ __forceinline__ bool wait_slot(const Shared<D>& sh, const Params& p, int it, int where) {
   using C = Cfg<D>;
   const uint32_t addr = sh.bar(C::kItemEmpty + it % kItems), parity = ((it / kItems) & 1) ^ 1;
-  if (__all_sync(0xffffffffu, mbar_try_wait(addr, parity))) return true;
   const int lane = threadIdx.x & 31;
-  uint32_t seen = 0;
-  uint64_t since = global_timer_ns();
+  uint32_t seen = ~0u;  // (no count of fills)
+  uint64_t since = 0;
 #pragma unroll 1
   while (!__all_sync(0xffffffffu, mbar_try_wait(addr, parity))) {
     if (__any_sync(0xffffffffu, sh.aborting())) return false;
