@@ -47,7 +47,7 @@ struct TablesParams {
   int32_t* ctok;   // partial-row index of each token, -1 for none
   wf_batch_ctok* ctok_list;  // and the tokens by that index
   int32_t B, max_tokens, cols, max_prefix, num_free, pool_pages;
-  int32_t page, page_shift, group, tile_tokens, block_tokens, kv_heads, max_ctas;
+  int32_t page, page_shift, tile_tokens, block_tokens, kv_heads, max_ctas;
   uint64_t fingerprint;
 };
 
@@ -545,7 +545,6 @@ extern "C" wf_status wf_batch_tables(const wf_batch_desc* desc, const int32_t* c
   p.pool_pages = desc->pool_pages;
   p.page = desc->page_tokens;
   while ((1 << p.page_shift) < p.page) ++p.page_shift;
-  p.group = L.group;
   p.tile_tokens = L.tile_tokens;
   p.block_tokens = desc->block_tokens;
   p.kv_heads = desc->num_kv_heads;
