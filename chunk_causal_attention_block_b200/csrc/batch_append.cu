@@ -11,8 +11,9 @@
 // threads as one token's rows or a few tokens' need, none idle: bytes in
 // flight are what the speed depends on (2.25 loads a thread in fixed blocks of
 // 256 reached 5.75 TB/s on 37440 tokens of 12 + 24 rows of 128, and 3.0 TB/s on
-// 16 + 2 rows of 64, where 14 of 32 row slots idled; now 6.3 TB/s on the
-// former, 112 us).  Neighbouring threads cover whole rows: coalesced.
+// 16 + 2 rows of 64, where 14 of 32 row slots idled; now 5.9 TB/s, 121 us, on
+// the former with other inputs every time, 6.3 TB/s, 112 us, on the same ones
+// again).  Neighbouring threads cover whole rows: coalesced.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

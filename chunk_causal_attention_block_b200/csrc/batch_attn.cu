@@ -34,11 +34,21 @@
 // columns wide.
 //
 // What bounds it.  Many single tokens: HBM (96 requests, up to 4000 own keys
-// each, 32760 shared, 12 heads: 250 us, 1.50 GB, 6.0 TB/s).  Long proposals:
-// the exponentials and MMAs of the two streams together, under the power limit
-// (2 x 4680 tokens over 42120 keys, 12 heads: 2.0-2.3 ms, 1.1-1.2 PFLOP/s of
-// visible pairs).  A few rows: latency (one token over 334 keys: 10 us, 4 of
-// them the merging's).
+// each, 32760 shared, 12 heads, 1.50 GB: 278 us, 5.4 TB/s, on other pages every
+// time; 250 us, 6.0 TB/s, on the same ones again).  Chunks of rows: the
+// exponentials and MMAs of the two streams, which are busy 57% of the time
+// each, under the power limit (2 x 4680 tokens over 42120 keys, 12 heads: 2.37
+// ms, 1.02 PFLOP/s of visible pairs with other inputs every time; 2.05-2.4 ms on
+// the same ones).  The stream attention (attn_sm100.cu) takes 7% less on a round
+// that both can run (18720 rows over up to 51480 keys, 12 heads, in turn on one
+// box: 5.1 and 5.5 ms); what makes the difference has not been measured.  A few
+// rows: latency (one token over 334 keys: 10 us, 4 of them the merging's).
+//
+// Precision.  Scores, maxima, sums, O and merged parts are fp32.  P is rounded
+// to bf16 for the product with V, since one tcgen05.mma takes both operands in
+// one 16-bit type and V's range needs bf16: a relative error over a case of
+// 0.0021-0.0023 against 64 bits, where an fp32 form that rounds O alone has
+// 0.0017.
 //
 // Warp roles (384 threads):
 //   warps 0-3, 4-7  softmax of stream 0 and 1
@@ -843,7 +853,8 @@ __device__ __forceinline__ void mma_issuer(const Shared<D>& sh, const Params& p,
 
 // ---------------------------------------------------------------- softmax
 // exp2(s * sl2 - m) as bf16 pairs into TMEM; returns the fp32 row sum (taken
-// before the rounding; P in bf16 feeds the tensor cores).
+// before the rounding, so that the errors of single weights average out instead
+// of moving the whole row).
 __device__ __forceinline__ float exp_to_p(const float (&s)[128], float sl2, float m_ref, uint32_t s_tm) {
   const float2 sl2x2 = make_float2(sl2, sl2);
   const float2 negm2 = make_float2(-m_ref, -m_ref);

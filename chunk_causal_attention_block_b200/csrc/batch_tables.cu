@@ -16,9 +16,14 @@
 // writes the per-request results and the work list, the others each take a
 // share of the new tokens and find a token's request by bisection in shared
 // memory.  A thread whose token opens a page writes that page's table entry,
-// so nobody reads an entry that somebody else writes.  Bound by latency (launch, scan, bisection), not by
-// its few bytes.  All sums are 64-bit; what does not fit voids the whole step
-// (no tokens, no work, tables untouched) and is recorded in the plan.
+// so nobody reads an entry that somebody else writes.  All sums are 64-bit; what
+// does not fit voids the whole step (no tokens, no work, tables untouched) and
+// is recorded in the plan.
+//
+// Not bound by its few bytes: up to about 1000 requests by latency (launch, scan,
+// bisection; a call in a graph 4.5 us for 5 and 64 requests, 6.1 for 512, 7.8 for
+// 1024), beyond that by block 0, which makes all units and finds where all
+// shares begin (10.9 us for 2048, 22 for 4096, 51 for 8192).
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -384,7 +384,7 @@ wf_status wf_chunk_causal_attn_fp8(const void* host_plan, const void* dev_plan, 
  * 128 tokens.  fp32 and other D return WF_ERR_UNSUPPORTED.
  */
 typedef struct wf_batch_desc {
-  int32_t num_heads;         /* H >= 1 */
+  int32_t num_heads;         /* H in [1, 4096] */
   int32_t num_kv_heads;      /* Hkv in [1, 256], divides H */
   int32_t head_dim;          /* D: 64 or 128 */
   int32_t dtype;             /* WF_BF16 */
