@@ -3,6 +3,7 @@ refusal names the argument and what is wrong with it, so that one check cannot
 stand in for another.  The plan is a raw address here (a tensor would have to
 be on a GPU), and nothing is ever launched: all memory is the host's."""
 import os
+import shutil
 import subprocess
 
 import pytest
@@ -135,6 +136,8 @@ def test_every_plan_holds_what_is_read_of_it_before_it_is_known_to_be_the_calls(
 
 
 def test_what_counts_as_shared_memory(tmp_path):
+    if not shutil.which("g++"):
+        pytest.skip("no C++ compiler")
     exe = str(tmp_path / "overlap")
     subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I", wfbuild.INCLUDE, "-I", wfbuild.CSRC,
                     os.path.join(os.path.dirname(__file__), "c", "overlap.cpp"), "-o", exe], check=True)

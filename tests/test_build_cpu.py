@@ -14,25 +14,48 @@ from chunk_causal_attention_block_b200 import wf
 
 
 @pytest.fixture
-def compiles(monkeypatch):
-    """Commands that the build would run, which are not."""
+def compiles(monkeypatch, tmp_path):
+    """Commands that the build would run, which are not; libraries lie in a folder of their own."""
     ran = []
     monkeypatch.setattr(subprocess, "run", lambda cmd, **kw: ran.append(cmd))
+    monkeypatch.setattr(wfbuild, "PKG", str(tmp_path))
     return ran
 
 
 def test_the_name_carries_the_versions(monkeypatch, compiles):
     lib = wfbuild.torch_lib()
     assert torch.__version__.replace("+", "-") in lib and sysconfig.get_config_var("SOABI") in lib and lib.endswith(".so")
-    assert os.path.exists(lib)
-    wfbuild.build()
-    assert not any(lib in cmd for cmd in compiles)  # up to date
+    wfbuild._build_torch_calls(False)
+    assert [lib in cmd for cmd in compiles] == [True]
+    with open(lib, "w"):
+        pass
+    wfbuild._build_torch_calls(False)
+    assert len(compiles) == 1  # newer than its sources
     # after an upgrade the one at hand is not taken for built
     monkeypatch.setattr(torch, "__version__", "99.0")
     other = wfbuild.torch_lib()
     assert other != lib
-    wfbuild.build()
-    assert [other in cmd for cmd in compiles] == [True]
+    wfbuild._build_torch_calls(False)
+    assert [other in cmd for cmd in compiles] == [False, True]
+
+
+@pytest.mark.parametrize("newer", ["TORCH_SRC", "a header", "the flags"])
+def test_it_is_built_again_for_what_it_is_made_of(monkeypatch, compiles, tmp_path, newer):
+    lib = wfbuild.torch_lib()
+    with open(lib, "w"):
+        pass
+    late = str(tmp_path / "newer")
+    with open(late, "w"):
+        pass
+    os.utime(late, (os.path.getmtime(lib) + 10,) * 2)
+    if newer == "TORCH_SRC":
+        monkeypatch.setattr(wfbuild, "TORCH_SRC", late)
+    elif newer == "a header":
+        monkeypatch.setattr(wfbuild, "_headers", lambda: [late])
+    else:
+        monkeypatch.setattr(wfbuild, "__file__", late)
+    wfbuild._build_torch_calls(False)
+    assert [lib in cmd for cmd in compiles] == [True]
 
 
 def test_a_library_for_another_torch_is_not_loaded(monkeypatch):
@@ -44,20 +67,21 @@ def test_a_library_for_another_torch_is_not_loaded(monkeypatch):
     assert wf._batch_calls() is not None
 
 
-def test_libwf_is_built_without_torch(monkeypatch, compiles, capsys):
+def test_no_torch_is_no_error(monkeypatch, compiles, capsys):
     monkeypatch.setitem(sys.modules, "torch", None)  # importing it fails
-    assert wfbuild.build() == wfbuild.LIB
+    wfbuild._build_torch_calls(False)
     assert "no torch" in capsys.readouterr().err and not compiles
 
 
-def test_libwf_is_built_without_gxx(monkeypatch, compiles, capsys):
-    monkeypatch.setattr(torch, "__version__", "99.0")  # (to be built, that is)
+def test_no_gxx_is_no_error(monkeypatch, compiles, capsys):
     monkeypatch.setattr(wfbuild.shutil, "which", lambda name: None)
-    assert wfbuild.build() == wfbuild.LIB
+    wfbuild._build_torch_calls(False)
     assert "no g++" in capsys.readouterr().err and not compiles
 
 
-def test_the_tensor_checks_can_be_left_out(monkeypatch, compiles):
-    monkeypatch.setattr(torch, "__version__", "99.0")
-    assert wfbuild.build(torch_calls=False) == wfbuild.LIB
-    assert not compiles
+def test_the_tensor_checks_can_be_left_out(monkeypatch):
+    wfbuild.build()  # (all else is up to date then)
+    asked = []
+    monkeypatch.setattr(wfbuild, "_build_torch_calls", asked.append)
+    assert wfbuild.build(torch_calls=False) == wfbuild.LIB and asked == []
+    assert wfbuild.build() == wfbuild.LIB and asked == [False]
