@@ -6,9 +6,10 @@ which checks torch tensors for the batch calls, with the host compiler.
 A C program needs libwf.so alone: the other is left out with --no-torch, and
 where there is no torch or no g++.  It reads the fields of torch's tensors
 inline, so its name carries the torch and the Python that it was built for, and
-one for others is neither loaded nor taken for up to date.  Objects go to ``_build/`` (git-ignored) and are rebuilt when a source or
-header is newer; the shared library lands next to this file so that it
-travels with the source tree.
+one for others is neither loaded nor taken for up to date.  Objects go to
+``_build/`` (git-ignored) and are rebuilt when a source or header is newer; the
+shared libraries land next to this file so that they travel with the source
+tree.
 """
 from __future__ import annotations
 

@@ -46,9 +46,8 @@
 //
 // Precision.  Scores, maxima, sums, O and merged parts are fp32.  P is rounded
 // to bf16 for the product with V, since one tcgen05.mma takes both operands in
-// one 16-bit type and V's range needs bf16: a relative error over a case of
-// 0.0021-0.0023 against 64 bits, where an fp32 form that rounds O alone has
-// 0.0017.
+// one 16-bit type and V is bf16: a relative error over a case of 0.0018-0.0024
+// against 64 bits, where an fp32 form that rounds O alone has 0.0016-0.0017.
 //
 // Warp roles (384 threads):
 //   warps 0-3, 4-7  softmax of stream 0 and 1
