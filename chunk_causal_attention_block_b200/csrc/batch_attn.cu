@@ -64,6 +64,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
@@ -1570,7 +1571,8 @@ __global__ void __launch_bounds__(kCombineThreads, 4) batch_combine_kernel(const
 
 // ---------------------------------------------------------------- host
 PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 fn = known.load(std::memory_order_relaxed);
   if (!fn) {
     void* ptr = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -1580,6 +1582,7 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
       return nullptr;
     }
     fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    known.store(fn, std::memory_order_relaxed);
   }
   return fn;
 }
@@ -1625,7 +1628,7 @@ std::mutex& between_kernels(const void* workspace) {
 template <int D>
 wf_status launch(const wf_batch_desc* d, const BatchLayout& L, const Params& p, const void* q, const void* k_pool,
                  const void* v_pool, cudaStream_t stream) {
-  static int attr_done[64] = {0};
+  static std::atomic<int> attr_done[64];  // (threads may find out the same at once)
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return WF_ERR_CUDA;
   if (dev < 0 || dev >= 64) return WF_ERR_UNSUPPORTED;

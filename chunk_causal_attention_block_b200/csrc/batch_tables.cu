@@ -26,6 +26,7 @@
 // shares begin (10.9 us for 2048, 22 for 4096, 51 for 8192).
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "wf_batch.h"
@@ -368,7 +369,7 @@ template <int kThreads>
 wf_status launch_tables(const TablesParams& p, cudaStream_t stream) {
   const size_t smem = sizeof(int32_t) * (4 * size_t(p.B) + 2);
   if (smem > 40 * 1024) {
-    static int attr_done[64] = {0};
+    static std::atomic<int> attr_done[64];  // (threads may find out the same at once)
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return WF_ERR_CUDA;
     if (dev < 0 || dev >= 64) return WF_ERR_UNSUPPORTED;
@@ -391,7 +392,7 @@ wf_status launch_tables(const TablesParams& p, cudaStream_t stream) {
 
 // SM count of the current device, asked for once per device.
 int sm_count() {
-  static int known[64] = {0};
+  static std::atomic<int> known[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
     cudaGetLastError();

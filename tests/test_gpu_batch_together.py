@@ -1,5 +1,8 @@
 """Batch calls beside one another: threads, graphs and plans that a program may
 share between them."""
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -146,3 +149,35 @@ def test_a_call_is_the_first_of_a_graph(call, before):
             continue
         assert torch.equal(s.out[:s.T], want["out"]) and torch.equal(s.lse[:, :s.T], want["lse"])
         assert (s.out[s.T:] == SENTINEL).all()
+
+
+def test_first_calls_of_a_process_may_come_from_many_threads():
+    # what a device's first call finds out and keeps (its size, the kernels' shared memory, the map encoder)
+    code = """
+import threading, torch
+from chunk_causal_attention_block_b200 import wf
+from tests.batch_common import Step
+kws = [dict(D=d, H=h, Hkv=h, seed=i) for i, (d, h) in enumerate([(64, 1), (128, 2)] * 4)]
+steps = [Step([40, 0] + [1] * 2600, [3, 150] + [0] * 2600, prefix=200, **kw) for kw in kws]
+torch.cuda.synchronize()
+failed, gate = [], threading.Barrier(len(steps))
+def work(s):
+    try:
+        s.stream = torch.cuda.Stream()
+        gate.wait()
+        s.run()
+        s.stream.synchronize()
+    except BaseException as e:
+        failed.append(e)
+threads = [threading.Thread(target=work, args=(s,)) for s in steps]
+[t.start() for t in threads]
+[t.join() for t in threads]
+assert not failed, failed
+for s in steps:
+    s.check_tables()
+    s.check_attention()
+print("all right")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.endswith("all right\n"), r.stderr[-2000:]
